@@ -33,6 +33,7 @@
 #include <vector>
 
 #include "fsdp_flat.h"
+#include "host.hpp"
 #include "plan.hpp"
 #include "tuning.hpp"
 
@@ -48,35 +49,7 @@ void fsdp_table_hook(int reduce, int elt, uint32_t n_items, uint64_t n_chunks, u
 
 namespace {
 
-thread_local std::string g_err;
-
-int fail(int code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  try {
-    g_err = buf;
-  } catch (...) {  // no memory for the message: the code still stands
-    g_err.clear();
-  }
-  return code;
-}
-
-int ok() {
-  g_err.clear();
-  return FSDP_OK;
-}
-
-constexpr int64_t kMaxBytes = int64_t(1) << 60;
-
-bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-  return !__builtin_mul_overflow(a, b, out) && *out <= kMaxBytes;
-}
-bool add_ok(int64_t a, int64_t b, int64_t* out) {
-  return !__builtin_add_overflow(a, b, out) && *out <= kMaxBytes;
-}
+using namespace fsdp::host;
 
 // Per parameter i sharded on dim k: outer = product of the dims before k,
 // dk = dim k, inner = product of the dims after k; rank s holds rows
@@ -151,15 +124,6 @@ int make_layout(const fsdp_bucket_t* b, int32_t S, Layout* L) {
   return FSDP_OK;
 }
 
-int elem_size(int32_t dtype) {
-  switch (dtype) {
-    case FSDP_F32: return 4;
-    case FSDP_BF16: return 2;
-    case FSDP_F16: return 2;
-    default: return 0;
-  }
-}
-
 // Element size of a reduction dtype: fp32, or bf16 / fp16 (summed in fp32).
 int reduce_elem_size(int32_t dtype) {
   return dtype == FSDP_F32 ? 4 : (dtype == FSDP_BF16 || dtype == FSDP_F16) ? 2 : 0;
@@ -168,41 +132,6 @@ int reduce_elem_size(int32_t dtype) {
 int check_groups(int32_t R, int32_t S) {
   if (R < 1 || S < 1) return fail(FSDP_EINVAL, "rank_size %d / shard_size %d must be >= 1", R, S);
   if (R % S != 0) return fail(FSDP_EINVAL, "rank_size %d is not a multiple of shard_size %d", R, S);
-  return FSDP_OK;
-}
-
-// ---------------------------------------------------------------------------
-// pointer checks
-// ---------------------------------------------------------------------------
-
-struct Span {
-  uint64_t a, b;  // [a, b)
-  int id;
-};
-
-int check_ptr(const void* p, int64_t nbytes, uint64_t align, const char* what, long idx) {
-  if (nbytes == 0) return FSDP_OK;
-  if (!p) return fail(FSDP_EINVAL, "%s[%ld] is NULL but holds %lld bytes", what, idx, (long long)nbytes);
-  if ((uint64_t)p % align)
-    return fail(FSDP_EALIGN, "%s[%ld] = %p is not %llu-byte aligned", what, idx, p, (unsigned long long)align);
-  return FSDP_OK;
-}
-
-// Outputs must be pairwise disjoint and disjoint from every input.
-int check_overlap(std::vector<Span> outs, const std::vector<Span>& ins) {
-  outs.erase(std::remove_if(outs.begin(), outs.end(), [](const Span& s) { return s.a == s.b; }), outs.end());
-  std::sort(outs.begin(), outs.end(), [](const Span& x, const Span& y) { return x.a < y.a; });
-  for (size_t k = 1; k < outs.size(); ++k)
-    if (outs[k].a < outs[k - 1].b)
-      return fail(FSDP_EOVERLAP, "output buffers %d and %d overlap", outs[k - 1].id, outs[k].id);
-  for (const Span& in : ins) {
-    if (in.a == in.b) continue;
-    // first output whose end is beyond in.a
-    auto it = std::upper_bound(outs.begin(), outs.end(), in.a,
-                               [](uint64_t v, const Span& s) { return v < s.b; });
-    if (it != outs.end() && it->a < in.b)
-      return fail(FSDP_EOVERLAP, "input buffer %d overlaps output buffer %d", in.id, it->id);
-  }
   return FSDP_OK;
 }
 
@@ -323,17 +252,6 @@ void drop_entry(std::list<Entry>::iterator it) {
   g_table_bytes -= it->plan.table_bytes();
   g_lru.erase(it);
 }
-
-// Is `stream` being captured into a HIP graph?
-bool capturing(hipStream_t stream) {
-  hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
-  return hipStreamIsCapturing(stream, &st) == hipSuccess && st == hipStreamCaptureStatusActive;
-}
-
-// Events the calling thread's next kernel launch records at its start and
-// end (fsdp_time_next_launch); taken by that launch.
-thread_local void* g_time_start = nullptr;
-thread_local void* g_time_stop = nullptr;
 
 int enqueue(const Plan& p, hipStream_t stream) {
   if (!p.launch && !p.fold_dev) return ok();
@@ -1450,24 +1368,6 @@ int fused_ar_impl(int32_t n_seg, const int64_t* seg_numel, int32_t rank_size, in
   }
   return run_reduce(std::move(key), jobs, ptrs, dtype, op == FSDP_AVG, Reuse::kFinal,
                     static_cast<hipStream_t>(stream));
-}
-
-// No C++ exception may cross the C ABI: host allocation failures while
-// planning become FSDP_ENOMEM, anything else FSDP_EINVAL.  Nothing has been
-// enqueued when an exception is thrown (launches come last).
-template <class F>
-int guarded(F&& f) noexcept {
-  try {
-    return f();
-  } catch (const std::bad_alloc&) {
-    return fail(FSDP_ENOMEM, "out of host memory while planning the call");
-  } catch (const std::length_error&) {
-    return fail(FSDP_ENOMEM, "the call's host tables would exceed the largest allocation");
-  } catch (const std::exception& e) {
-    return fail(FSDP_EINVAL, "internal error: %s", e.what());
-  } catch (...) {
-    return fail(FSDP_EINVAL, "internal error");
-  }
 }
 
 }  // namespace
