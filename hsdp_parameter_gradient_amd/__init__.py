@@ -32,6 +32,17 @@ from ._binding import (  # noqa: F401
 )
 from .flat_bucket import FlatBucket, FusedGroup  # noqa: F401
 from .pipeline import BackwardPipeline  # noqa: F401
+from .token_ops import (  # noqa: F401
+    LAYER,
+    RMS,
+    Dropout,
+    fsdp_embedding,
+    fsdp_embedding_grad,
+    fsdp_embedding_grad_workspace,
+    fsdp_norm,
+    fsdp_norm_grad,
+    fsdp_norm_grad_workspace,
+)
 
 __all__ = [
     "FlatBucket", "FusedGroup", "BackwardPipeline",
@@ -40,5 +51,7 @@ __all__ = [
     "fsdp_last_error", "fsdp_release_cache", "fsdp_rs_copy_in", "fsdp_rs_copy_reduce",
     "fsdp_rs_copy_reduce_noalloc", "fsdp_rs_reduce",
     "fsdp_time_next_launch",
+    "LAYER", "RMS", "Dropout", "fsdp_embedding", "fsdp_embedding_grad", "fsdp_embedding_grad_workspace",
+    "fsdp_norm", "fsdp_norm_grad", "fsdp_norm_grad_workspace",
     "lib", "lib_path", "prepare",
 ]

@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_int32, c_int64, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_uint32, c_void_p
 from typing import List, NamedTuple, Optional, Sequence, Tuple
 
 import torch
@@ -42,6 +42,10 @@ class _Bucket(ctypes.Structure):
     _fields_ = [("n_params", c_int32), ("ndim", POINTER(c_int32)),
                 ("shape", POINTER(c_int64)), ("shard_dim", c_int32),
                 ("shard_dims", POINTER(c_int32))]
+
+
+class _Dropout(ctypes.Structure):
+    _fields_ = [("p", c_double), ("site", c_uint32), ("state", c_void_p)]
 
 
 _LIB = None
@@ -77,6 +81,18 @@ def lib() -> ctypes.CDLL:
                                             POINTER(c_void_p), c_void_p],
             "fsdp_fused_ar": [c_int32, P64, c_int32, c_int32, c_int32, c_int32, c_int32,
                               POINTER(c_void_p), c_void_p],
+            "fsdp_embedding": [c_int64, c_int64, c_int32, c_int32, c_void_p, c_int64, c_int32, c_void_p, c_float,
+                               POINTER(_Dropout), c_void_p, c_void_p],
+            "fsdp_embedding_grad_workspace": [c_int32, c_int64, c_int64, c_int64, P64],
+            "fsdp_embedding_grad": [c_int32, c_int64, c_int64, c_int32, c_int32, c_int64, c_int32, c_void_p, c_void_p,
+                                    c_float, POINTER(_Dropout), c_int32, POINTER(c_void_p), c_void_p, c_int64,
+                                    c_void_p],
+            "fsdp_norm": [c_int32, c_int64, c_int64, c_int32, c_int32, c_void_p, c_void_p, POINTER(_Dropout), c_void_p,
+                          c_void_p, c_float, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p],
+            "fsdp_norm_grad_workspace": [c_int32, c_int64, c_int64, P64],
+            "fsdp_norm_grad": [c_int32, c_int32, c_int64, c_int64, c_int32, c_int32, c_int32, c_void_p, c_void_p,
+                               c_void_p, c_void_p, c_void_p, c_void_p, POINTER(_Dropout), c_int32, c_void_p, c_void_p,
+                               POINTER(c_void_p), POINTER(c_void_p), c_void_p, c_int64, c_void_p],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -410,11 +426,11 @@ _PREP = {
 }
 
 
-def prepare(fn, *args) -> _Call:
+def prepare(fn, *args, **kwargs) -> _Call:
     """Check and marshal the arguments of device entry point `fn` (a name
     or one of this module's functions) once; the result issues the call."""
     name = fn if isinstance(fn, str) else fn.__name__
-    return _PREP[name](*args)
+    return _PREP[name](*args, **kwargs)
 
 
 def fsdp_ag_copy_in(shapes, shard_size: int, shards: Sequence[torch.Tensor], ag: torch.Tensor,

@@ -17,6 +17,8 @@ import re
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -28,14 +30,13 @@ _REMARK = "kernel-resource-usage"
 _FIELDS = {"VGPRs": "vgprs", "AGPRs": "agprs", "TotalSGPRs": "sgprs", "ScratchSize [bytes/lane]": "scratch_bytes",
            "Occupancy [waves/SIMD]": "waves_per_simd", "VGPRs Spill": "vgpr_spill", "SGPRs Spill": "sgpr_spill",
            "LDS Size [bytes/block]": "lds_bytes"}
-SOURCES = ("fsdp_flat.cpp", "kernels.hip")
+SOURCES = ("fsdp_flat.cpp", "kernels.hip", "token_ops.cpp", "token_kernels.hip")
 
 HIP_FLAGS = [
     "--offload-arch=gfx950",
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-Wall",
     # IEEE fp32 everywhere: keep denormals, correctly rounded division
     "-fno-gpu-flush-denormals-to-zero",
@@ -75,22 +76,33 @@ def build(verbose: bool = False) -> str:
     os.makedirs(LIB_DIR, exist_ok=True)
     out = os.path.join(LIB_DIR, LIB_NAME)
     tmp = out + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *HIP_FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-           *[os.path.join(CSRC, s) for s in SOURCES], "-o", tmp, "-Rpass-analysis=" + _REMARK]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        return subprocess.run(cmd, capture_output=True, text=True)
+
+    with tempfile.TemporaryDirectory() as objs:
+        obj = {s: os.path.join(objs, s + ".o") for s in SOURCES}
+        with ThreadPoolExecutor(len(SOURCES)) as pool:  # one compiler per source
+            rs = list(pool.map(lambda s: run([hipcc(), *HIP_FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC,
+                                              "-c", os.path.join(CSRC, s), "-o", obj[s],
+                                              "-Rpass-analysis=" + _REMARK]), SOURCES))
+        if all(r.returncode == 0 for r in rs):
+            rs.append(run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *obj.values(), "-o", tmp]))
+    stderr = "\n".join(r.stderr or "" for r in rs)
     # hipcc's host pass does not know the packed-fp32 feature and says so
     noise = "not a recognized feature for this target"
-    warn = "\n".join(l for l in (r.stderr or "").splitlines()
+    warn = "\n".join(l for l in stderr.splitlines()
                      if noise not in l and "ignoring feature" not in l and _REMARK not in l)
-    if r.returncode != 0:
+    failed = [r for r in rs if r.returncode != 0]
+    if failed:
         if os.path.exists(tmp):
             os.unlink(tmp)
-        raise RuntimeError("hipcc failed (%d):\n%s\n%s" % (r.returncode, r.stdout, warn))
+        raise RuntimeError("hipcc failed (%d):\n%s\n%s" % (failed[0].returncode, failed[0].stdout, warn))
     if verbose and warn.strip():
         print(warn, file=sys.stderr)
-    res = parse_resources(r.stderr or "")
+    res = parse_resources(stderr)
     rtmp = os.path.join(LIB_DIR, RESOURCES + ".tmp%d" % os.getpid())
     with open(rtmp, "w") as f:
         json.dump(res, f, indent=1, sort_keys=True)

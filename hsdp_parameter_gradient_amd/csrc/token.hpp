@@ -1,0 +1,115 @@
+// Arguments of the token operators' kernels (embedding, norm and their
+// gradients), shared by the host entry points and the gfx950 launchers.
+//
+// Activations are dense rows of `cols` elements.  A row is cut into groups of
+// 8 columns (kGroup), the unit of the kernels' loads and of the dropout's
+// generator; the last group of a row may be short.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+namespace fsdp {
+
+constexpr uint32_t kGroup = 8;
+
+// Gradient pointers carried in a launch's kernel arguments; calls of more
+// ranks launch the kernels that write gradients once per kMaxRankPtrs ranks.
+constexpr int kMaxRankPtrs = 64;
+struct RankPtrs {
+  void* p[kMaxRankPtrs];
+};
+
+// Dropout behind a lookup or before a residual add; state == nullptr: none.
+struct Drop {
+  const uint64_t* state;  // device: {seed, step}
+  uint32_t cut;           // an element is dropped where its 16 random bits are below this
+  uint32_t site;
+};
+
+struct EmbedArgs {
+  const void* table;
+  const void* tokens;
+  void* out;
+  uint64_t n_tokens, vocab, cols;
+  float factor;  // scale, times 65536 / (65536 - cut) with a dropout
+  int table_dtype, out_dtype, token_bytes;
+  Drop drop;
+};
+
+// The gradient's workspace, per rank g (u32 words, then floats):
+//   off[V + 1]    off[v]..off[v + 1]: the sorted positions of token v
+//   order[T]      the rank's positions with a valid token, ascending by
+//                 token, positions of one token ascending
+//   part[2 * pieces][cols]  partial sums of tokens with many positions
+constexpr uint32_t kPiece = 64;  // sorted positions per partial sum
+constexpr uint32_t kLong = 64;   // a token with more positions is summed in pieces
+static_assert(kLong >= kPiece, "at most two long tokens may meet a piece, the second one its end");
+
+struct EmbedGradArgs {
+  const void* tokens;  // [n_ranks, n_tokens]
+  const void* dout;    // [n_ranks * n_tokens, cols]
+  void* const* grads;  // host array of n_ranks device pointers
+  uint32_t* off;
+  uint32_t* order;
+  float* part;
+  uint64_t n_tokens, vocab, cols;
+  float factor;
+  int n_ranks, dtype, grad_dtype, token_bytes, accumulate;
+  Drop drop;
+};
+
+struct NormArgs {
+  const void* x;
+  const void* residual;  // nullptr: none
+  const void* weight;
+  const void* bias;  // nullptr: none
+  void* h;           // nullptr: not written (x is the norm's input)
+  void* y;
+  float* mean;  // nullptr: not written
+  float* rstd;  // nullptr: not written
+  uint64_t rows, cols;
+  float eps, factor;
+  int rms, dtype, weight_dtype;
+  Drop drop;
+};
+
+struct NormGradArgs {
+  const void* dy;
+  const void* dh;  // nullptr: none
+  const void* h;
+  const float* mean;  // nullptr: zero (rms)
+  const float* rstd;
+  const void* weight;
+  void* dres;
+  void* dx;  // nullptr: not written
+  void* const* dweight;
+  void* const* dbias;  // nullptr: none
+  float* part;         // [n_ranks][blocks][1 or 2][cols]
+  uint64_t rows, cols;  // rows of one rank
+  float factor;
+  int n_ranks, blocks, rms, dtype, weight_dtype, grad_dtype, accumulate;
+  Drop drop;
+};
+
+// Workgroups per rank of the norm gradient's first kernel (and so its
+// partial sums per rank): a function of the sizes only, so that the order of
+// every sum is fixed.
+int norm_grad_blocks(uint64_t rows, uint64_t cols, int n_ranks);
+
+// Whether the launches of a call stay within the largest grid.
+bool grid_fits(uint64_t blocks, uint32_t block);
+bool embedding_fits(uint64_t n_tokens, uint64_t cols);
+bool embedding_grad_fits(uint64_t n_tokens, uint64_t vocab, uint64_t cols);
+
+}  // namespace fsdp
+
+// Launchers (token_kernels.hip).  Return hipSuccess or the launch error.
+// start_event / stop_event: recorded by the call's first and last dispatch,
+// or NULL.
+extern "C++" {
+int fsdp_launch_embedding(const fsdp::EmbedArgs& a, void* stream, void* start_event, void* stop_event);
+int fsdp_launch_embedding_grad(const fsdp::EmbedGradArgs& a, void* stream, void* start_event, void* stop_event);
+int fsdp_launch_norm(const fsdp::NormArgs& a, void* stream, void* start_event, void* stop_event);
+int fsdp_launch_norm_grad(const fsdp::NormGradArgs& a, void* stream, void* start_event, void* stop_event);
+}

@@ -1,0 +1,1172 @@
+// gfx950 kernels of the token operators: embedding lookup and norm with their
+// gradients, and the dropout inside them.
+//
+// Every kernel is a stream over rows of activations: a lane holds groups of 8
+// neighbouring columns, sums are fp32, each output is rounded once.  Rows
+// need no alignment beyond their element's: groups are loaded and stored with
+// 16-byte accesses at element alignment (the target's global memory accesses
+// may be unaligned), and only a row's short last group goes element by
+// element.
+
+#include <hip/hip_ext.h>
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fsdp_flat.h"
+#include "token.hpp"
+
+namespace {
+
+#define GMEM __attribute__((address_space(1)))
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+// the same vectors at their elements' alignment
+typedef f32x4 f32x4e __attribute__((aligned(4)));
+typedef u32x4 u32x4e __attribute__((aligned(2)));
+typedef u32x2 u32x2e __attribute__((aligned(2)));
+
+constexpr uint32_t kGroup = fsdp::kGroup;
+
+template <typename T>
+__device__ __forceinline__ GMEM T* gmem(const void* p) {
+  return reinterpret_cast<GMEM T*>(reinterpret_cast<uint64_t>(p));
+}
+
+// --- elements ---------------------------------------------------------------
+
+// One element of dtype D as float, and back (rounded to nearest even).
+template <int D>
+struct Elem;
+template <>
+struct Elem<FSDP_F32> {
+  typedef float T;
+  static __device__ __forceinline__ float get(float x) { return x; }
+  static __device__ __forceinline__ float put(float x) { return x; }
+};
+template <>
+struct Elem<FSDP_BF16> {
+  typedef uint16_t T;
+  static __device__ __forceinline__ float get(uint16_t x) { return __builtin_bit_cast(float, (uint32_t)x << 16); }
+  static __device__ __forceinline__ uint16_t put(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
+};
+template <>
+struct Elem<FSDP_F16> {
+  typedef uint16_t T;
+  static __device__ __forceinline__ float get(uint16_t x) { return (float)__builtin_bit_cast(_Float16, x); }
+  static __device__ __forceinline__ uint16_t put(float x) { return __builtin_bit_cast(uint16_t, (_Float16)x); }
+};
+
+template <int D>
+__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b) {
+  if constexpr (D == FSDP_BF16) {
+    a = __builtin_bit_cast(float, w << 16);
+    b = __builtin_bit_cast(float, w & 0xFFFF0000u);
+  } else {
+    const f16x2 h = __builtin_bit_cast(f16x2, w);
+    a = (float)h[0];
+    b = (float)h[1];
+  }
+}
+
+template <int D>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const f32x2 v = {a, b};
+  if constexpr (D == FSDP_BF16)
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+  else
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+}
+
+// N (4 or 8) columns of dtype D from element `at` of base; only the first
+// `n` exist (the others read as zero).
+template <int D, int N>
+__device__ __forceinline__ void load_cols(const void* base, uint64_t at, uint32_t n, float (&v)[N]) {
+  typedef typename Elem<D>::T T;
+  const GMEM T* p = gmem<T>(base) + at;
+  if (n >= N) {
+    if constexpr (D == FSDP_F32) {
+#pragma unroll
+      for (int k = 0; k < N; k += 4) {
+        const f32x4 w = *reinterpret_cast<const GMEM f32x4e*>(p + k);
+        v[k] = w[0], v[k + 1] = w[1], v[k + 2] = w[2], v[k + 3] = w[3];
+      }
+    } else if constexpr (N == 8) {
+      const u32x4 w = *reinterpret_cast<const GMEM u32x4e*>(p);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) unpack2<D>(w[k], v[2 * k], v[2 * k + 1]);
+    } else {
+      const u32x2 w = *reinterpret_cast<const GMEM u32x2e*>(p);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) unpack2<D>(w[k], v[2 * k], v[2 * k + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = (uint32_t)k < n ? Elem<D>::get(p[k]) : 0.0f;
+  }
+}
+
+template <int D, int N>
+__device__ __forceinline__ void store_cols(void* base, uint64_t at, uint32_t n, const float (&v)[N]) {
+  typedef typename Elem<D>::T T;
+  GMEM T* p = gmem<T>(base) + at;
+  if (n >= N) {
+    if constexpr (D == FSDP_F32) {
+#pragma unroll
+      for (int k = 0; k < N; k += 4) *reinterpret_cast<GMEM f32x4e*>(p + k) = f32x4{v[k], v[k + 1], v[k + 2], v[k + 3]};
+    } else if constexpr (N == 8) {
+      u32x4 w;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = pack2<D>(v[2 * k], v[2 * k + 1]);
+      *reinterpret_cast<GMEM u32x4e*>(p) = w;
+    } else {
+      *reinterpret_cast<GMEM u32x2e*>(p) = u32x2{pack2<D>(v[0], v[1]), pack2<D>(v[2], v[3])};
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if ((uint32_t)k < n) p[k] = Elem<D>::put(v[k]);
+  }
+}
+
+// The same for a dtype known at run time only (the same for every lane).
+template <int N>
+__device__ __forceinline__ void load_any(int dtype, const void* base, uint64_t at, uint32_t n, float (&v)[N]) {
+  if (dtype == FSDP_F32)
+    load_cols<FSDP_F32, N>(base, at, n, v);
+  else if (dtype == FSDP_BF16)
+    load_cols<FSDP_BF16, N>(base, at, n, v);
+  else
+    load_cols<FSDP_F16, N>(base, at, n, v);
+}
+
+template <int N>
+__device__ __forceinline__ void store_any(int dtype, void* base, uint64_t at, uint32_t n, const float (&v)[N]) {
+  if (dtype == FSDP_F32)
+    store_cols<FSDP_F32, N>(base, at, n, v);
+  else if (dtype == FSDP_BF16)
+    store_cols<FSDP_BF16, N>(base, at, n, v);
+  else
+    store_cols<FSDP_F16, N>(base, at, n, v);
+}
+
+__device__ __forceinline__ int64_t token_at(const void* tokens, uint64_t i, int bytes) {
+  return bytes == 8 ? gmem<int64_t>(tokens)[i] : (int64_t)gmem<int32_t>(tokens)[i];
+}
+
+// --- dropout ------------------------------------------------------------------
+
+// Philox4x32 with 7 rounds, the fewest that pass BigCrush (Salmon, Moraes,
+// Dror, Shaw: "Parallel random numbers: as easy as 1, 2, 3", SC 2011): 128
+// random bits for the 8 columns of one group, 16 each.  Counter (group, row,
+// site, step), key = seed.  One 32 x 32 -> 64 bit multiply per half round.
+__device__ __forceinline__ u32x4 random_bits(uint32_t group, uint32_t row, uint32_t site, uint32_t step,
+                                             uint32_t k0, uint32_t k1) {
+  uint32_t c0 = group, c1 = row, c2 = site, c3 = step;
+#pragma unroll
+  for (int r = 0; r < 7; ++r) {
+    const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c1 = (uint32_t)b;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c3 = (uint32_t)a;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return u32x4{c0, c1, c2, c3};
+}
+
+// The generator's state of one call, read once per workgroup.
+struct Rng {
+  uint32_t k0, k1, site, step, cut;
+};
+
+__device__ __forceinline__ Rng rng_of(const fsdp::Drop& d) {
+  const GMEM uint64_t* s = gmem<uint64_t>(d.state);
+  const uint64_t seed = s[0], step = s[1];
+  return Rng{(uint32_t)seed, (uint32_t)(seed >> 32), d.site, (uint32_t)step, d.cut};
+}
+
+// Zero the dropped elements of a row's columns [8 * group + half, + N): a
+// select, so that a dropped infinity or NaN leaves nothing behind.
+template <int N>
+__device__ __forceinline__ void drop_cols(const Rng& g, uint32_t row, uint32_t group, uint32_t half, float (&v)[N]) {
+  const u32x4 w = random_bits(group, row, g.site, g.step, g.k0, g.k1);
+  if constexpr (N == 8) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t u = k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu;
+      v[k] = u < g.cut ? 0.0f : v[k];
+    }
+  } else {
+    const uint32_t a = half ? w[2] : w[0], b = half ? w[3] : w[1];
+    v[0] = (a & 0xFFFFu) < g.cut ? 0.0f : v[0];
+    v[1] = (a >> 16) < g.cut ? 0.0f : v[1];
+    v[2] = (b & 0xFFFFu) < g.cut ? 0.0f : v[2];
+    v[3] = (b >> 16) < g.cut ? 0.0f : v[3];
+  }
+}
+
+// --- splitting a flat range of (row, group) items -------------------------------
+
+// A workgroup takes kItems consecutive items; item i belongs to row
+// i / groups.  Only the workgroup's first item needs a 64-bit division; the
+// rest is q / groups for q < groups + kItems: by a multiply with the rounded-up
+// reciprocal (exact while q * groups < 2^32), or one compare where a row is
+// longer than kItems.
+struct Split {
+  uint64_t row0;
+  uint32_t rem, groups, recip;
+
+  __device__ __forceinline__ void at(uint32_t i, uint64_t& row, uint32_t& group) const {
+    const uint32_t q = rem + i;
+    uint32_t d;
+    if (groups == 1)
+      d = q;
+    else if (recip)
+      d = __umulhi(q, recip);
+    else
+      d = q >= groups;
+    row = row0 + d;
+    group = q - d * groups;
+  }
+};
+
+constexpr uint32_t kMaxRecipGroups = 32768;  // (groups + kItems) * groups < 2^32
+
+__device__ __forceinline__ Split split_of(uint64_t first, uint32_t groups, uint32_t recip) {
+  const uint64_t row = first / groups;
+  return Split{row, (uint32_t)(first - row * groups), groups, recip};
+}
+
+uint32_t recip_of(uint64_t groups) {
+  return groups > 1 && groups <= kMaxRecipGroups ? (uint32_t)((uint64_t(1) << 32) / groups + 1) : 0;
+}
+
+// --- embedding ------------------------------------------------------------------
+
+// out[t] = drop(factor * table[token[t]]): one pass, bound by reading the
+// rows looked up and writing the output.  A lane moves kEmbedUnroll groups.
+constexpr int kEmbedBlock = 256;
+constexpr int kEmbedUnroll = 4;
+
+template <int TD, int OD, bool DROP>
+__global__ __launch_bounds__(kEmbedBlock) void embedding_kernel(fsdp::EmbedArgs a, uint32_t groups, uint32_t recip) {
+  constexpr uint32_t kItems = kEmbedBlock * kEmbedUnroll;
+  const uint64_t first = (uint64_t)blockIdx.x * kItems;
+  const uint64_t n = a.n_tokens * groups;
+  const Split sp = split_of(first, groups, recip);
+  Rng rng;
+  if constexpr (DROP) rng = rng_of(a.drop);
+  float v[kEmbedUnroll][8];
+  uint64_t row[kEmbedUnroll];
+  uint32_t grp[kEmbedUnroll], len[kEmbedUnroll];
+#pragma unroll
+  for (int u = 0; u < kEmbedUnroll; ++u) {
+    const uint32_t i = u * kEmbedBlock + threadIdx.x;
+    sp.at(i, row[u], grp[u]);
+    len[u] = 0;
+    if (first + i < n) {
+      const uint64_t left = a.cols - (uint64_t)grp[u] * kGroup;
+      len[u] = left < kGroup ? (uint32_t)left : kGroup;
+      const int64_t tok = token_at(a.tokens, row[u], a.token_bytes);
+      const bool in = tok >= 0 && (uint64_t)tok < a.vocab;
+      load_cols<TD, 8>(a.table, in ? (uint64_t)tok * a.cols + (uint64_t)grp[u] * kGroup : 0, in ? len[u] : 0, v[u]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kEmbedUnroll; ++u) {
+    if (!len[u]) continue;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[u][k] *= a.factor;
+    if constexpr (DROP) drop_cols<8>(rng, (uint32_t)row[u], grp[u], 0, v[u]);
+    store_cols<OD, 8>(a.out, row[u] * a.cols + (uint64_t)grp[u] * kGroup, len[u], v[u]);
+  }
+}
+
+// --- embedding gradient: the positions sorted by token ------------------------
+
+// One workgroup per kSortRows tokens and rank.  It reads all of the rank's
+// tokens twice (from L2), counts those of its own tokens and those below
+// them, and so knows where its part of the order begins without waiting for
+// another workgroup.  Each of its waves has a contiguous part of the
+// positions and counts apart, so that positions of one token stay ascending:
+// the order, and with it every sum, is the same on every run.
+constexpr int kSortBlock = 1024;
+constexpr int kSortWaves = kSortBlock / 64;
+constexpr uint32_t kSortRows = 512;
+
+__global__ __launch_bounds__(kSortBlock) void token_sort_kernel(const void* tokens, int token_bytes, uint64_t n_tokens,
+                                                                uint64_t vocab, uint32_t* off, uint32_t* order) {
+  __shared__ uint32_t cnt[kSortWaves][kSortRows];
+  __shared__ uint32_t lower, wave_sum[kSortRows / 64];
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint64_t g = blockIdx.y;
+  const uint64_t v0 = (uint64_t)blockIdx.x * kSortRows;
+  const uint32_t rows = vocab - v0 < kSortRows ? (uint32_t)(vocab - v0) : kSortRows;
+  for (uint32_t i = tid; i < kSortWaves * kSortRows; i += kSortBlock) (&cnt[0][0])[i] = 0;
+  if (tid == 0) lower = 0;
+  __syncthreads();
+  // this wave's positions
+  const uint64_t per = ((n_tokens + kSortBlock - 1) / kSortBlock) * 64;
+  const uint64_t begin = wave * per, end = begin + per < n_tokens ? begin + per : n_tokens;
+  const uint64_t tok0 = g * n_tokens;
+  uint32_t low = 0;
+  for (uint64_t t = begin + lane; t < end; t += 64) {
+    const int64_t tok = token_at(tokens, tok0 + t, token_bytes);
+    const uint64_t r = (uint64_t)tok - v0;  // wraps for a token below v0
+    low += tok >= 0 && (uint64_t)tok < v0;
+    if (tok >= 0 && (uint64_t)tok >= v0 && r < rows) atomicAdd(&cnt[wave][r], 1u);
+  }
+#pragma unroll
+  for (int s = 32; s; s >>= 1) low += __shfl_xor(low, s);
+  if (lane == 0 && low) atomicAdd(&lower, low);
+  __syncthreads();
+  // exclusive prefix over the tokens, then over the waves of each token
+  uint32_t total = 0, incl = 0;
+  if (tid < kSortRows) {
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) total += cnt[w][tid];
+    incl = total;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const uint32_t up = __shfl_up(incl, s);
+      if (lane >= (uint32_t)s) incl += up;
+    }
+    if (lane == 63) wave_sum[wave] = incl;
+  }
+  __syncthreads();
+  if (tid < kSortRows) {
+    uint32_t at = lower + incl - total;
+    for (uint32_t w = 0; w < wave; ++w) at += wave_sum[w];
+    uint32_t* o = off + g * (vocab + 1) + v0;
+    if (tid < rows) o[tid] = at;
+    if (v0 + rows == vocab && tid == rows - 1) o[rows] = at + total;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t c = cnt[w][tid];
+      cnt[w][tid] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  for (uint64_t t0 = begin; t0 < end; t0 += 64) {
+    const uint64_t t = t0 + lane;
+    int64_t tok = -1;
+    if (t < end) tok = token_at(tokens, tok0 + t, token_bytes);
+    const uint64_t r64 = (uint64_t)tok - v0;
+    const bool mine = tok >= 0 && (uint64_t)tok >= v0 && r64 < rows;
+    const uint32_t r = mine ? (uint32_t)r64 : ~0u;
+    uint64_t todo = __ballot(mine);
+    while (todo) {
+      const int lead = __ffsll((unsigned long long)todo) - 1;
+      const uint32_t row = __shfl(r, lead);
+      const uint64_t same = __ballot(r == row);
+      uint32_t at = 0;
+      if (lane == (uint32_t)lead) at = atomicAdd(&cnt[wave][row], (uint32_t)__popcll(same));
+      at = __shfl(at, lead);
+      if (r == row) order[g * n_tokens + at + __popcll(same & ((uint64_t(1) << lane) - 1))] = (uint32_t)t;
+      todo &= ~same;
+    }
+  }
+}
+
+// What the summing kernels see of one rank.
+struct RankView {
+  const GMEM uint32_t* off;
+  const GMEM uint32_t* order;
+  uint64_t row0;  // the rank's first row of dout
+};
+
+__device__ __forceinline__ RankView rank_view(const fsdp::EmbedGradArgs& a, uint64_t g) {
+  return RankView{gmem<uint32_t>(a.off) + g * (a.vocab + 1), gmem<uint32_t>(a.order) + g * a.n_tokens,
+                  g * a.n_tokens};
+}
+
+constexpr int kCols = 4;  // columns of a lane in the summing kernels: 16-byte fp32 stores
+
+// sum over sorted positions [b, e) of columns [c, c + 4) of dout, ascending
+template <int D, bool DROP>
+__device__ __forceinline__ void sum_positions(const fsdp::EmbedGradArgs& a, const RankView& rv, const Rng& rng,
+                                              uint32_t b, uint32_t e, uint64_t c, uint32_t len, float (&acc)[kCols]) {
+  uint32_t k = b;
+  for (; k + 4 <= e; k += 4) {
+    float v[4][kCols];
+    uint64_t row[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      row[u] = rv.row0 + rv.order[k + u];
+      load_cols<D, kCols>(a.dout, row[u] * a.cols + c, len, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if constexpr (DROP) drop_cols<kCols>(rng, (uint32_t)row[u], (uint32_t)(c / kGroup), c & 4, v[u]);
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) acc[i] += v[u][i];
+    }
+  }
+  for (; k < e; ++k) {
+    float v[kCols];
+    const uint64_t row = rv.row0 + rv.order[k];
+    load_cols<D, kCols>(a.dout, row * a.cols + c, len, v);
+    if constexpr (DROP) drop_cols<kCols>(rng, (uint32_t)row, (uint32_t)(c / kGroup), c & 4, v);
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) acc[i] += v[i];
+  }
+}
+
+// factor * acc into (or added to) columns [c, c + 4) of row v of a gradient
+__device__ __forceinline__ void put_grad(const fsdp::EmbedGradArgs& a, void* grad, uint64_t v, uint64_t c,
+                                         uint32_t len, const float (&acc)[kCols]) {
+  float out[kCols];
+  if (a.accumulate) {
+    load_any<kCols>(a.grad_dtype, grad, v * a.cols + c, len, out);
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) out[i] += a.factor * acc[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) out[i] = a.factor * acc[i];
+  }
+  store_any<kCols>(a.grad_dtype, grad, v * a.cols + c, len, out);
+}
+
+// The first `row_blocks` workgroups of a rank take (row, 4 columns) items: a
+// row of the gradient whose token has at most kLong positions is summed and
+// written at once, rows without a position included (they are written as
+// zeros).  When the gradient is added to, rows without a position stay as
+// they are, and the items are the sorted positions instead: the one that is
+// its token's first does the row.  The other workgroups sum the tokens with
+// more than kLong positions in pieces of kPiece sorted positions into `part`
+// (slot 0: the piece's first token, slot 1: its last, where that is another).
+constexpr int kGradBlock = 256;
+constexpr int kGradUnroll = 4;
+
+template <int D, bool DROP>
+__global__ __launch_bounds__(kGradBlock) void embedding_grad_kernel(fsdp::EmbedGradArgs a, fsdp::RankPtrs grads,
+                                                                    uint32_t rank0, uint32_t row_blocks,
+                                                                    uint32_t col_blocks, uint32_t groups,
+                                                                    uint32_t recip) {
+  const uint64_t g = rank0 + blockIdx.y;
+  const RankView rv = rank_view(a, g);
+  Rng rng;
+  if constexpr (DROP) rng = rng_of(a.drop);
+  if (blockIdx.x < row_blocks) {
+    constexpr uint32_t kItems = kGradBlock * kGradUnroll;
+    const uint64_t first = (uint64_t)blockIdx.x * kItems;
+    const uint64_t n = (a.accumulate ? rv.off[a.vocab] : a.vocab) * groups;
+    if (first >= n) return;
+    const Split sp = split_of(first, groups, recip);
+#pragma unroll
+    for (int u = 0; u < kGradUnroll; ++u) {
+      const uint32_t i = u * kGradBlock + threadIdx.x;
+      if (first + i >= n) break;
+      uint64_t v;
+      uint32_t j;
+      sp.at(i, v, j);
+      uint64_t at = v;
+      if (a.accumulate) {
+        v = (uint64_t)token_at(a.tokens, rv.row0 + rv.order[at], a.token_bytes);
+        if (rv.off[v] != at) continue;
+      }
+      const uint32_t b = rv.off[v], e = rv.off[v + 1];
+      if (e - b > fsdp::kLong) continue;
+      const uint64_t c = (uint64_t)j * kCols;
+      const uint32_t len = a.cols - c < kCols ? (uint32_t)(a.cols - c) : kCols;
+      float acc[kCols] = {};
+      sum_positions<D, DROP>(a, rv, rng, b, e, c, len, acc);
+      put_grad(a, grads.p[blockIdx.y], v, c, len, acc);
+    }
+    return;
+  }
+  const uint32_t k = blockIdx.x - row_blocks;
+  const uint32_t piece = k / col_blocks;
+  const uint64_t c = ((uint64_t)(k - piece * col_blocks) * kGradBlock + threadIdx.x) * kCols;
+  const uint32_t valid = rv.off[a.vocab];
+  const uint32_t k0 = piece * fsdp::kPiece;
+  if (k0 >= valid || c >= a.cols) return;
+  const uint32_t k1 = valid - k0 < fsdp::kPiece ? valid : k0 + fsdp::kPiece;
+  const uint32_t len = a.cols - c < kCols ? (uint32_t)(a.cols - c) : kCols;
+  const uint64_t pieces = (a.n_tokens + fsdp::kPiece - 1) / fsdp::kPiece;
+  float* part = a.part + (g * pieces + piece) * 2 * a.cols;
+  const uint64_t va = (uint64_t)token_at(a.tokens, rv.row0 + rv.order[k0], a.token_bytes);
+  const uint64_t vb = (uint64_t)token_at(a.tokens, rv.row0 + rv.order[k1 - 1], a.token_bytes);
+  const uint32_t ea = rv.off[va + 1];
+  if (ea - rv.off[va] > fsdp::kLong) {
+    float acc[kCols] = {};
+    sum_positions<D, DROP>(a, rv, rng, k0, ea < k1 ? ea : k1, c, len, acc);
+    store_cols<FSDP_F32, kCols>(part, c, len, acc);
+  }
+  const uint32_t bb = rv.off[vb];
+  if (vb != va && rv.off[vb + 1] - bb > fsdp::kLong) {
+    float acc[kCols] = {};
+    sum_positions<D, DROP>(a, rv, rng, bb, k1, c, len, acc);
+    store_cols<FSDP_F32, kCols>(part + a.cols, c, len, acc);
+  }
+}
+
+// Joins the pieces of the tokens with more than kLong positions.  Such a
+// token reaches past the piece it begins in, so it is that piece's last one:
+// the workgroups of the piece (64 lanes x 4 columns each) add its partial
+// sums, every fourth to a wave, and the four waves' sums in a fixed order.
+__global__ __launch_bounds__(256) void embedding_join_kernel(fsdp::EmbedGradArgs a, fsdp::RankPtrs grads,
+                                                             uint32_t rank0, uint32_t col_blocks) {
+  __shared__ float sums[4][64 * kCols];
+  const uint64_t g = rank0 + blockIdx.y;
+  const RankView rv = rank_view(a, g);
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t piece = blockIdx.x / col_blocks;
+  const uint64_t c = ((uint64_t)(blockIdx.x - piece * col_blocks) * 64 + lane) * kCols;
+  const uint32_t valid = rv.off[a.vocab];
+  const uint32_t k0 = piece * fsdp::kPiece;
+  if (k0 >= valid) return;
+  const uint32_t k1 = valid - k0 < fsdp::kPiece ? valid : k0 + fsdp::kPiece;
+  const uint64_t v = (uint64_t)token_at(a.tokens, rv.row0 + rv.order[k1 - 1], a.token_bytes);
+  const uint32_t b = rv.off[v], e = rv.off[v + 1];
+  if (e - b <= fsdp::kLong || b < k0) return;  // the same for the whole workgroup
+  const uint32_t last = (e - 1) / fsdp::kPiece;
+  const uint64_t pieces = (a.n_tokens + fsdp::kPiece - 1) / fsdp::kPiece;
+  const float* part = a.part + g * pieces * 2 * a.cols;
+  const uint32_t len = c >= a.cols ? 0 : a.cols - c < kCols ? (uint32_t)(a.cols - c) : kCols;
+  float acc[kCols] = {};
+  if (len) {
+    for (uint32_t q = piece + wave; q <= last; q += 4) {
+      float p[kCols];
+      const uint64_t slot = 2 * (uint64_t)q + (q == piece && b > k0);
+      load_cols<FSDP_F32, kCols>(part, slot * a.cols + c, len, p);
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) acc[i] += p[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) sums[wave][lane * kCols + i] = acc[i];
+  __syncthreads();
+  if (wave == 0 && len) {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+      const uint32_t s = lane * kCols + i;
+      acc[i] = (sums[0][s] + sums[1][s]) + (sums[2][s] + sums[3][s]);
+    }
+    put_grad(a, grads.p[blockIdx.y], v, c, len, acc);
+  }
+}
+
+// --- sums over a row ------------------------------------------------------------
+
+// LANES lanes hold one row (16, 64, or a whole workgroup of 256, 512 or 1024):
+// the sums of `a` and `b` over the row, in every one of its lanes.  `slot`
+// alternates between calls, so that one barrier per call is enough.
+template <int LANES>
+__device__ __forceinline__ void row_sum2(float& a, float& b, float (*lds)[2][LANES < 64 ? 1 : LANES / 64], int slot) {
+#pragma unroll
+  for (int s = (LANES < 64 ? LANES : 64) / 2; s; s >>= 1) {
+    a += __shfl_xor(a, s);
+    b += __shfl_xor(b, s);
+  }
+  if constexpr (LANES > 64) {
+    constexpr int W = LANES / 64;
+    if ((threadIdx.x & 63) == 0) {
+      lds[slot][0][threadIdx.x >> 6] = a;
+      lds[slot][1][threadIdx.x >> 6] = b;
+    }
+    __syncthreads();
+    a = b = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      a += lds[slot][0][w];
+      b += lds[slot][1][w];
+    }
+  }
+}
+
+// --- norm -----------------------------------------------------------------------
+
+constexpr int block_of(int lanes) { return lanes < 256 ? 256 : lanes; }
+
+// h = residual + drop(x), rounded to the activations' type (the norm and its
+// gradient see the same h); y = (h - mean) * rstd * weight + bias.  LANES
+// lanes keep a row in registers, NV groups each, so that x and the residual
+// are read once.  The variance is the mean square of h - mean, less the
+// square of what rounding the mean left: a row far from zero loses nothing.
+template <int D, int LANES, int NV, bool DROP>
+__global__ __launch_bounds__(block_of(LANES)) void norm_kernel(fsdp::NormArgs a, uint32_t groups) {
+  constexpr int kRows = block_of(LANES) / LANES;
+  __shared__ float lds[2][2][LANES < 64 ? 1 : LANES / 64];
+  const uint32_t l = threadIdx.x % LANES;
+  Rng rng;
+  if constexpr (DROP) rng = rng_of(a.drop);
+  const float inv = 1.0f / (float)a.cols;
+  int slot = 0;
+  for (uint64_t row = (uint64_t)blockIdx.x * kRows + threadIdx.x / LANES; row < a.rows;
+       row += (uint64_t)gridDim.x * kRows) {
+    float v[NV][8];
+    uint32_t len[NV];
+    const uint64_t at = row * a.cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t j = l + i * LANES;
+      len[i] = j >= groups ? 0 : a.cols - (uint64_t)j * kGroup < kGroup ? (uint32_t)(a.cols - (uint64_t)j * kGroup) : kGroup;
+      load_cols<D, 8>(a.x, len[i] ? at + (uint64_t)j * kGroup : 0, len[i], v[i]);
+    }
+    if (a.h) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const uint32_t j = l + i * LANES;
+        if (!len[i]) continue;
+        if constexpr (DROP) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[i][k] *= a.factor;
+          drop_cols<8>(rng, (uint32_t)row, j, 0, v[i]);
+        }
+        if (a.residual) {
+          float r[8];
+          load_cols<D, 8>(a.residual, at + (uint64_t)j * kGroup, len[i], r);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[i][k] += r[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] = Elem<D>::get(Elem<D>::put(v[i][k]));
+        store_cols<D, 8>(a.h, at + (uint64_t)j * kGroup, len[i], v[i]);
+      }
+    }
+    float mean = 0.0f, sum = 0.0f, sq = 0.0f;
+    if (!a.rms) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum += v[i][k];
+      row_sum2<LANES>(sum, sq, lds, slot);
+      slot ^= 1;
+      mean = sum * inv;
+      sum = sq = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float d = (uint32_t)k < len[i] ? v[i][k] - mean : 0.0f;
+        v[i][k] = d;
+        sum += d;
+        sq += d * d;
+      }
+    row_sum2<LANES>(sum, sq, lds, slot);
+    slot ^= 1;
+    const float rest = a.rms ? 0.0f : sum * inv;
+    const float rstd = 1.0f / sqrtf((sq * inv - rest * rest) + a.eps);
+    if (l == 0) {
+      if (a.mean) a.mean[row] = mean + rest;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t j = l + i * LANES;
+      if (!len[i]) continue;
+      float w[8];
+      load_any<8>(a.weight_dtype, a.weight, (uint64_t)j * kGroup, len[i], w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[i][k] = (v[i][k] - rest) * rstd * w[k];
+      if (a.bias) {
+        load_any<8>(a.weight_dtype, a.bias, (uint64_t)j * kGroup, len[i], w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] += w[k];
+      }
+      store_cols<D, 8>(a.y, at + (uint64_t)j * kGroup, len[i], v[i]);
+    }
+  }
+}
+
+// Rows too long for registers: h (or x) is read three times, the second and
+// third time mostly from L2.
+template <int D, bool DROP>
+__global__ __launch_bounds__(1024) void norm_wide_kernel(fsdp::NormArgs a, uint32_t groups) {
+  constexpr int LANES = 1024;
+  __shared__ float lds[2][2][LANES / 64];
+  Rng rng;
+  if constexpr (DROP) rng = rng_of(a.drop);
+  const float inv = 1.0f / (float)a.cols;
+  const void* in = a.h ? a.h : a.x;
+  auto len_of = [&](uint32_t j) {
+    const uint64_t left = a.cols - (uint64_t)j * kGroup;
+    return left < kGroup ? (uint32_t)left : kGroup;
+  };
+  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const uint64_t at = row * a.cols;
+    float sum = 0.0f, sq = 0.0f, v[8];
+    for (uint32_t j = threadIdx.x; j < groups; j += LANES) {
+      const uint32_t len = len_of(j);
+      const uint64_t p = at + (uint64_t)j * kGroup;
+      load_cols<D, 8>(a.x, p, len, v);
+      if (a.h) {
+        if constexpr (DROP) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] *= a.factor;
+          drop_cols<8>(rng, (uint32_t)row, j, 0, v);
+        }
+        if (a.residual) {
+          float r[8];
+          load_cols<D, 8>(a.residual, p, len, r);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] += r[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = Elem<D>::get(Elem<D>::put(v[k]));
+        store_cols<D, 8>(a.h, p, len, v);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum += v[k];
+    }
+    // a lane reads back only what it stored itself
+    row_sum2<LANES>(sum, sq, lds, 0);
+    const float mean = a.rms ? 0.0f : sum * inv;
+    sum = sq = 0.0f;
+    for (uint32_t j = threadIdx.x; j < groups; j += LANES) {
+      const uint32_t len = len_of(j);
+      load_cols<D, 8>(in, at + (uint64_t)j * kGroup, len, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float d = (uint32_t)k < len ? v[k] - mean : 0.0f;
+        sum += d;
+        sq += d * d;
+      }
+    }
+    row_sum2<LANES>(sum, sq, lds, 1);
+    const float rest = a.rms ? 0.0f : sum * inv;
+    const float rstd = 1.0f / sqrtf((sq * inv - rest * rest) + a.eps);
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[row] = mean + rest;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    for (uint32_t j = threadIdx.x; j < groups; j += LANES) {
+      const uint32_t len = len_of(j);
+      const uint64_t p = at + (uint64_t)j * kGroup;
+      float w[8];
+      load_cols<D, 8>(in, p, len, v);
+      load_any<8>(a.weight_dtype, a.weight, (uint64_t)j * kGroup, len, w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = ((v[k] - mean) - rest) * rstd * w[k];
+      if (a.bias) {
+        load_any<8>(a.weight_dtype, a.bias, (uint64_t)j * kGroup, len, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += w[k];
+      }
+      store_cols<D, 8>(a.y, p, len, v);
+    }
+  }
+}
+
+// --- norm gradient ----------------------------------------------------------------
+
+// With xhat = (h - mean) * rstd and g = dy * weight, row by row:
+//   dres = rstd * (g - mean(g) - xhat * mean(g * xhat)) + dh
+//   dx   = drop'(dres)
+// (rms: without mean(g)), and over a rank's rows dweight = sum dy * xhat,
+// dbias = sum dy.  A lane keeps the same columns in every row, so the two
+// column sums stay in its registers; a workgroup writes them once, as one row
+// of `part`, after its waves' sums were added in LDS in a fixed order.
+template <int D, int LANES, int NV, bool DROP>
+__global__ __launch_bounds__(block_of(LANES)) void norm_grad_kernel(fsdp::NormGradArgs a, uint32_t groups) {
+  constexpr int kBlockSize = block_of(LANES);
+  constexpr int kRows = kBlockSize / LANES;
+  constexpr uint32_t kWidth = LANES * NV * kGroup;  // columns the lanes of a row cover
+  __shared__ float lds[2][2][LANES < 64 ? 1 : LANES / 64];
+  __shared__ float cross[kRows > 1 ? kRows * kWidth : 1];
+  const uint32_t l = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+  const uint64_t g = blockIdx.y;
+  Rng rng;
+  if constexpr (DROP) rng = rng_of(a.drop);
+  const float inv = 1.0f / (float)a.cols;
+  float w[NV][8], dw[NV][8] = {}, db[NV][8] = {};
+  uint32_t len[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const uint32_t j = l + i * LANES;
+    len[i] = j >= groups ? 0 : a.cols - (uint64_t)j * kGroup < kGroup ? (uint32_t)(a.cols - (uint64_t)j * kGroup) : kGroup;
+    load_any<8>(a.weight_dtype, a.weight, len[i] ? (uint64_t)j * kGroup : 0, len[i], w[i]);
+  }
+  int slot = 0;
+  for (uint64_t r = (uint64_t)blockIdx.x * kRows + sub; r < a.rows; r += (uint64_t)gridDim.x * kRows) {
+    const uint64_t row = g * a.rows + r, at = row * a.cols;
+    float x[NV][8], dy[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint64_t p = len[i] ? at + (uint64_t)(l + i * LANES) * kGroup : 0;
+      load_cols<D, 8>(a.h, p, len[i], x[i]);
+      load_cols<D, 8>(a.dy, p, len[i], dy[i]);
+    }
+    const float mean = a.mean ? a.mean[row] : 0.0f, rstd = a.rstd[row];
+    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float xh = (uint32_t)k < len[i] ? (x[i][k] - mean) * rstd : 0.0f;
+        dw[i][k] += dy[i][k] * xh;
+        db[i][k] += dy[i][k];
+        const float gw = dy[i][k] * w[i][k];
+        x[i][k] = xh;
+        dy[i][k] = gw;
+        s0 += gw;
+        s1 += gw * xh;
+      }
+    row_sum2<LANES>(s0, s1, lds, slot);
+    slot ^= 1;
+    const float m0 = a.rms ? 0.0f : s0 * inv, m1 = s1 * inv;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (!len[i]) continue;
+      const uint32_t j = l + i * LANES;
+      const uint64_t p = at + (uint64_t)j * kGroup;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[i][k] = rstd * ((dy[i][k] - m0) - x[i][k] * m1);
+      if (a.dh) {
+        float t[8];
+        load_cols<D, 8>(a.dh, p, len[i], t);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[i][k] += t[k];
+      }
+      store_cols<D, 8>(a.dres, p, len[i], x[i]);
+      if (a.dx) {
+        if constexpr (DROP) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[i][k] *= a.factor;
+          drop_cols<8>(rng, (uint32_t)row, j, 0, x[i]);
+        }
+        store_cols<D, 8>(a.dx, p, len[i], x[i]);
+      }
+    }
+  }
+  const uint32_t sums = a.dbias ? 2 : 1;
+  float* part = a.part + ((g * gridDim.x + blockIdx.x) * sums) * a.cols;
+  for (uint32_t s = 0; s < sums; ++s) {
+    float(&acc)[NV][8] = s ? db : dw;
+    if constexpr (kRows > 1) {
+      if (s) __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) cross[sub * kWidth + (l + i * LANES) * kGroup + k] = acc[i][k];
+      __syncthreads();
+      for (uint32_t c = threadIdx.x; c < a.cols; c += kBlockSize) {
+        float t = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) t += cross[q * kWidth + c];
+        part[s * a.cols + c] = t;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (len[i]) store_cols<FSDP_F32, 8>(part, s * a.cols + (uint64_t)(l + i * LANES) * kGroup, len[i], acc[i]);
+    }
+  }
+}
+
+// Rows too long for registers: two passes over the row, the column sums kept
+// in the workgroup's own rows of `part` (a lane reads back only what it wrote).
+template <int D, bool DROP>
+__global__ __launch_bounds__(1024) void norm_grad_wide_kernel(fsdp::NormGradArgs a, uint32_t groups) {
+  constexpr int LANES = 1024;
+  __shared__ float lds[2][2][LANES / 64];
+  const uint64_t g = blockIdx.y;
+  Rng rng;
+  if constexpr (DROP) rng = rng_of(a.drop);
+  const float inv = 1.0f / (float)a.cols;
+  const uint32_t sums = a.dbias ? 2 : 1;
+  float* part = a.part + ((g * gridDim.x + blockIdx.x) * sums) * a.cols;
+  int slot = 0;
+  auto len_of = [&](uint32_t j) {
+    const uint64_t left = a.cols - (uint64_t)j * kGroup;
+    return left < kGroup ? (uint32_t)left : kGroup;
+  };
+  const float zero[8] = {};
+  for (uint32_t j = threadIdx.x; j < groups; j += LANES)
+    for (uint32_t s = 0; s < sums; ++s)
+      store_cols<FSDP_F32, 8>(part, s * a.cols + (uint64_t)j * kGroup, len_of(j), zero);
+  for (uint64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const uint64_t row = g * a.rows + r, at = row * a.cols;
+    const float mean = a.mean ? a.mean[row] : 0.0f, rstd = a.rstd[row];
+    float s0 = 0.0f, s1 = 0.0f;
+    for (uint32_t j = threadIdx.x; j < groups; j += LANES) {
+      const uint32_t len = len_of(j);
+      const uint64_t p = at + (uint64_t)j * kGroup;
+      float x[8], dy[8], w[8], t[8];
+      load_cols<D, 8>(a.h, p, len, x);
+      load_cols<D, 8>(a.dy, p, len, dy);
+      load_any<8>(a.weight_dtype, a.weight, (uint64_t)j * kGroup, len, w);
+      load_cols<FSDP_F32, 8>(part, (uint64_t)j * kGroup, len, t);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float xh = (uint32_t)k < len ? (x[k] - mean) * rstd : 0.0f;
+        t[k] += dy[k] * xh;
+        const float gw = dy[k] * w[k];
+        s0 += gw;
+        s1 += gw * xh;
+      }
+      store_cols<FSDP_F32, 8>(part, (uint64_t)j * kGroup, len, t);
+      if (a.dbias) {
+        load_cols<FSDP_F32, 8>(part, a.cols + (uint64_t)j * kGroup, len, t);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t[k] += dy[k];
+        store_cols<FSDP_F32, 8>(part, a.cols + (uint64_t)j * kGroup, len, t);
+      }
+    }
+    row_sum2<LANES>(s0, s1, lds, slot);
+    slot ^= 1;
+    const float m0 = a.rms ? 0.0f : s0 * inv, m1 = s1 * inv;
+    for (uint32_t j = threadIdx.x; j < groups; j += LANES) {
+      const uint32_t len = len_of(j);
+      const uint64_t p = at + (uint64_t)j * kGroup;
+      float x[8], dy[8], w[8];
+      load_cols<D, 8>(a.h, p, len, x);
+      load_cols<D, 8>(a.dy, p, len, dy);
+      load_any<8>(a.weight_dtype, a.weight, (uint64_t)j * kGroup, len, w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = rstd * ((dy[k] * w[k] - m0) - (x[k] - mean) * rstd * m1);
+      if (a.dh) {
+        load_cols<D, 8>(a.dh, p, len, dy);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] += dy[k];
+      }
+      store_cols<D, 8>(a.dres, p, len, x);
+      if (a.dx) {
+        if constexpr (DROP) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] *= a.factor;
+          drop_cols<8>(rng, (uint32_t)row, j, 0, x);
+        }
+        store_cols<D, 8>(a.dx, p, len, x);
+      }
+    }
+  }
+}
+
+// A rank's dweight (and dbias): the column sums of its `blocks` partial rows.
+// A workgroup takes 64 columns of one of the two: 16 waves add every
+// sixteenth partial row, then the waves' sums in a fixed order.
+constexpr int kJoinWaves = 16;
+
+__global__ __launch_bounds__(kJoinWaves * 64) void norm_join_kernel(fsdp::NormGradArgs a, fsdp::RankPtrs dweight,
+                                                                    fsdp::RankPtrs dbias, uint32_t rank0) {
+  __shared__ float lds[kJoinWaves][64];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint64_t g = rank0 + blockIdx.y, c = (uint64_t)blockIdx.x * 64 + lane;
+  const uint32_t s = blockIdx.z, sums = gridDim.z;
+  const float* part = a.part + (g * a.blocks * sums + s) * a.cols;
+  float t = 0.0f;
+  if (c < a.cols)
+    for (uint32_t b = wave; b < (uint32_t)a.blocks; b += kJoinWaves) t += gmem<float>(part)[(uint64_t)b * sums * a.cols + c];
+  lds[wave][lane] = t;
+  __syncthreads();
+  if (wave == 0 && c < a.cols) {
+    t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWaves; ++w) t += lds[w][lane];
+    void* out = s ? dbias.p[blockIdx.y] : dweight.p[blockIdx.y];
+    float v[1] = {t};
+    if (a.grad_dtype == FSDP_F32) {
+      GMEM float* p = gmem<float>(out) + c;
+      *p = a.accumulate ? *p + v[0] : v[0];
+    } else {
+      GMEM uint16_t* p = gmem<uint16_t>(out) + c;
+      if (a.grad_dtype == FSDP_BF16)
+        *p = Elem<FSDP_BF16>::put(a.accumulate ? Elem<FSDP_BF16>::get(*p) + v[0] : v[0]);
+      else
+        *p = Elem<FSDP_F16>::put(a.accumulate ? Elem<FSDP_F16>::get(*p) + v[0] : v[0]);
+    }
+  }
+}
+
+// --- launches -------------------------------------------------------------------
+
+struct Launch {
+  hipStream_t stream;
+  hipEvent_t start, stop;
+
+  template <typename... KArgs, typename... Args>
+  int operator()(void (*kernel)(KArgs...), dim3 grid, int block, bool first, bool last, Args... args) const {
+    hipEvent_t e0 = first ? start : nullptr, e1 = last ? stop : nullptr;
+    if (e0 || e1)
+      hipExtLaunchKernelGGL(kernel, grid, dim3(block), 0, stream, e0, e1, 0, args...);
+    else
+      hipLaunchKernelGGL(kernel, grid, dim3(block), 0, stream, args...);
+    return (int)hipGetLastError();
+  }
+};
+
+uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+Launch launch_of(void* stream, void* start, void* stop) {
+  return Launch{static_cast<hipStream_t>(stream), static_cast<hipEvent_t>(start), static_cast<hipEvent_t>(stop)};
+}
+
+template <int TD, int OD>
+int embedding_go(const Launch& go, const fsdp::EmbedArgs& a) {
+  const uint64_t groups = ceil_div(a.cols, kGroup);
+  const dim3 grid((uint32_t)ceil_div(a.n_tokens * groups, kEmbedBlock * kEmbedUnroll));
+  if (a.drop.state)
+    return go(embedding_kernel<TD, OD, true>, grid, kEmbedBlock, true, true, a, (uint32_t)groups, recip_of(groups));
+  return go(embedding_kernel<TD, OD, false>, grid, kEmbedBlock, true, true, a, (uint32_t)groups, recip_of(groups));
+}
+
+template <int TD>
+int embedding_table(const Launch& go, const fsdp::EmbedArgs& a) {
+  switch (a.out_dtype) {
+    case FSDP_F32: return embedding_go<TD, FSDP_F32>(go, a);
+    case FSDP_BF16: return embedding_go<TD, FSDP_BF16>(go, a);
+    default: return embedding_go<TD, FSDP_F16>(go, a);
+  }
+}
+
+template <int D, int LANES, int NV>
+int norm_rows(const Launch& go, const fsdp::NormArgs& a, uint32_t groups) {
+  constexpr uint64_t rows = block_of(LANES) / LANES;
+  const uint64_t need = ceil_div(a.rows, rows);
+  const uint64_t cap = 256 * 16;
+  const dim3 grid((uint32_t)(need < cap ? need : cap));
+  if (a.drop.state) return go(norm_kernel<D, LANES, NV, true>, grid, block_of(LANES), true, true, a, groups);
+  return go(norm_kernel<D, LANES, NV, false>, grid, block_of(LANES), true, true, a, groups);
+}
+
+template <int D>
+int norm_go(const Launch& go, const fsdp::NormArgs& a) {
+  const uint32_t groups = (uint32_t)ceil_div(a.cols, kGroup);
+  if (groups <= 16) return norm_rows<D, 16, 1>(go, a, groups);
+  if (groups <= 64) return norm_rows<D, 64, 1>(go, a, groups);
+  if (groups <= 128) return norm_rows<D, 64, 2>(go, a, groups);
+  if (groups <= 256) return norm_rows<D, 256, 1>(go, a, groups);
+  if (groups <= 512) return norm_rows<D, 256, 2>(go, a, groups);
+  if (groups <= 1024) return norm_rows<D, 512, 2>(go, a, groups);
+  if (groups <= 2048) return norm_rows<D, 1024, 2>(go, a, groups);
+  const dim3 grid((uint32_t)(a.rows < 1024 ? a.rows : 1024));
+  if (a.drop.state) return go(norm_wide_kernel<D, true>, grid, 1024, true, true, a, groups);
+  return go(norm_wide_kernel<D, false>, grid, 1024, true, true, a, groups);
+}
+
+template <int D, int LANES, int NV>
+int norm_grad_rows(const Launch& go, const fsdp::NormGradArgs& a, uint32_t groups) {
+  const dim3 grid((uint32_t)a.blocks, (uint32_t)a.n_ranks);
+  if (a.drop.state) return go(norm_grad_kernel<D, LANES, NV, true>, grid, block_of(LANES), true, false, a, groups);
+  return go(norm_grad_kernel<D, LANES, NV, false>, grid, block_of(LANES), true, false, a, groups);
+}
+
+template <int D>
+int norm_grad_go(const Launch& go, const fsdp::NormGradArgs& a) {
+  const uint32_t groups = (uint32_t)ceil_div(a.cols, kGroup);
+  if (groups <= 16) return norm_grad_rows<D, 16, 1>(go, a, groups);
+  if (groups <= 64) return norm_grad_rows<D, 64, 1>(go, a, groups);
+  if (groups <= 128) return norm_grad_rows<D, 64, 2>(go, a, groups);
+  if (groups <= 256) return norm_grad_rows<D, 256, 1>(go, a, groups);
+  if (groups <= 512) return norm_grad_rows<D, 256, 2>(go, a, groups);
+  if (groups <= 1024) return norm_grad_rows<D, 512, 2>(go, a, groups);
+  const dim3 grid((uint32_t)a.blocks, (uint32_t)a.n_ranks);
+  if (a.drop.state) return go(norm_grad_wide_kernel<D, true>, grid, 1024, true, false, a, groups);
+  return go(norm_grad_wide_kernel<D, false>, grid, 1024, true, false, a, groups);
+}
+
+template <int D, bool DROP>
+int embedding_grad_go(const Launch& go, const fsdp::EmbedGradArgs& a) {
+  int rc = go(token_sort_kernel, dim3((uint32_t)ceil_div(a.vocab, kSortRows), (uint32_t)a.n_ranks), kSortBlock, true,
+              false, a.tokens, a.token_bytes, a.n_tokens, a.vocab, a.off, a.order);
+  if (rc) return rc;
+  const uint64_t groups = ceil_div(a.cols, kCols);
+  const uint64_t row_blocks = ceil_div((a.accumulate ? a.n_tokens : a.vocab) * groups, kGradBlock * kGradUnroll);
+  const bool pieces = a.n_tokens > fsdp::kLong;  // else no token has more positions
+  const uint64_t n_pieces = pieces ? ceil_div(a.n_tokens, fsdp::kPiece) : 0;
+  const uint64_t cb = ceil_div(a.cols, kGradBlock * kCols), cj = ceil_div(a.cols, 64 * kCols);
+  for (int g0 = 0; g0 < a.n_ranks; g0 += fsdp::kMaxRankPtrs) {
+    const int n = a.n_ranks - g0 < fsdp::kMaxRankPtrs ? a.n_ranks - g0 : fsdp::kMaxRankPtrs;
+    const bool end = g0 + n == a.n_ranks;
+    fsdp::RankPtrs ptrs = {};
+    for (int k = 0; k < n; ++k) ptrs.p[k] = a.grads[g0 + k];
+    rc = go(embedding_grad_kernel<D, DROP>, dim3((uint32_t)(row_blocks + n_pieces * cb), (uint32_t)n), kGradBlock,
+            false, end && !pieces, a, ptrs, (uint32_t)g0, (uint32_t)row_blocks, (uint32_t)cb, (uint32_t)groups,
+            recip_of(groups));
+    if (rc) return rc;
+    if (pieces) {
+      rc = go(embedding_join_kernel, dim3((uint32_t)(n_pieces * cj), (uint32_t)n), 256, false, end, a, ptrs,
+              (uint32_t)g0, (uint32_t)cj);
+      if (rc) return rc;
+    }
+  }
+  return 0;
+}
+
+template <int D>
+int embedding_grad_drop(const Launch& go, const fsdp::EmbedGradArgs& a) {
+  return a.drop.state ? embedding_grad_go<D, true>(go, a) : embedding_grad_go<D, false>(go, a);
+}
+
+}  // namespace
+
+// Enough workgroups to fill the chip over all ranks, and at least one row for
+// each of a workgroup's rows in flight.
+int fsdp::norm_grad_blocks(uint64_t rows, uint64_t cols, int n_ranks) {
+  const uint64_t in_flight = cols <= 128 ? 16 : cols <= 1024 ? 4 : 1;
+  const uint64_t most = ceil_div(512, (uint64_t)n_ranks), need = ceil_div(rows, in_flight);
+  return (int)(need < 1 ? 1 : need < most ? need : most);
+}
+
+// The largest grid: HIP counts a dimension's threads in 32 bits.
+bool fsdp::grid_fits(uint64_t blocks, uint32_t block) { return blocks <= 0xFFFFFFFFull / block; }
+
+bool fsdp::embedding_fits(uint64_t n_tokens, uint64_t cols) {
+  return grid_fits(ceil_div(n_tokens * ceil_div(cols, kGroup), kEmbedBlock * kEmbedUnroll), kEmbedBlock);
+}
+
+bool fsdp::embedding_grad_fits(uint64_t n_tokens, uint64_t vocab, uint64_t cols) {
+  const uint64_t rows = vocab > n_tokens ? vocab : n_tokens, pieces = ceil_div(n_tokens, kPiece);
+  return grid_fits(ceil_div(vocab, kSortRows), kSortBlock) &&
+         grid_fits(ceil_div(rows * ceil_div(cols, kCols), kGradBlock * kGradUnroll) +
+                       pieces * ceil_div(cols, kGradBlock * kCols), kGradBlock) &&
+         grid_fits(pieces * ceil_div(cols, 64 * kCols), 256);
+}
+
+int fsdp_launch_embedding(const fsdp::EmbedArgs& a, void* stream, void* start_event, void* stop_event) {
+  const Launch go = launch_of(stream, start_event, stop_event);
+  switch (a.table_dtype) {
+    case FSDP_F32: return embedding_table<FSDP_F32>(go, a);
+    case FSDP_BF16: return embedding_table<FSDP_BF16>(go, a);
+    default: return embedding_table<FSDP_F16>(go, a);
+  }
+}
+
+int fsdp_launch_embedding_grad(const fsdp::EmbedGradArgs& a, void* stream, void* start_event, void* stop_event) {
+  const Launch go = launch_of(stream, start_event, stop_event);
+  switch (a.dtype) {
+    case FSDP_F32: return embedding_grad_drop<FSDP_F32>(go, a);
+    case FSDP_BF16: return embedding_grad_drop<FSDP_BF16>(go, a);
+    default: return embedding_grad_drop<FSDP_F16>(go, a);
+  }
+}
+
+int fsdp_launch_norm(const fsdp::NormArgs& a, void* stream, void* start_event, void* stop_event) {
+  const Launch go = launch_of(stream, start_event, stop_event);
+  switch (a.dtype) {
+    case FSDP_F32: return norm_go<FSDP_F32>(go, a);
+    case FSDP_BF16: return norm_go<FSDP_BF16>(go, a);
+    default: return norm_go<FSDP_F16>(go, a);
+  }
+}
+
+int fsdp_launch_norm_grad(const fsdp::NormGradArgs& a, void* stream, void* start_event, void* stop_event) {
+  const Launch go = launch_of(stream, start_event, stop_event);
+  int rc;
+  switch (a.dtype) {
+    case FSDP_F32: rc = norm_grad_go<FSDP_F32>(go, a); break;
+    case FSDP_BF16: rc = norm_grad_go<FSDP_BF16>(go, a); break;
+    default: rc = norm_grad_go<FSDP_F16>(go, a); break;
+  }
+  for (int g0 = 0; !rc && g0 < a.n_ranks; g0 += fsdp::kMaxRankPtrs) {
+    const int n = a.n_ranks - g0 < fsdp::kMaxRankPtrs ? a.n_ranks - g0 : fsdp::kMaxRankPtrs;
+    fsdp::RankPtrs w = {}, b = {};
+    for (int k = 0; k < n; ++k) {
+      w.p[k] = a.dweight[g0 + k];
+      if (a.dbias) b.p[k] = a.dbias[g0 + k];
+    }
+    rc = go(norm_join_kernel, dim3((uint32_t)ceil_div(a.cols, 64), (uint32_t)n, a.dbias ? 2 : 1), kJoinWaves * 64, false,
+            g0 + n == a.n_ranks, a, w, b, (uint32_t)g0);
+  }
+  return rc;
+}

@@ -1,0 +1,384 @@
+// Host side of the token operators (embedding lookup and norm with their
+// gradients): argument validation, workspace layout and the extern "C" entry
+// points declared in include/fsdp_flat.h.  These calls have no descriptor
+// tables and no cached plans: every argument travels with the launch, so any
+// call can be captured into a HIP graph, its first one included.
+
+#include <hip/hip_runtime_api.h>
+
+#include <cmath>
+#include <vector>
+
+#include "fsdp_flat.h"
+#include "host.hpp"
+#include "token.hpp"
+
+namespace {
+
+using namespace fsdp::host;
+
+constexpr int64_t kMaxRows = int64_t(1) << 31;  // rows and tokens of one call, columns, vocabulary
+constexpr int32_t kMaxRanks = 65535;            // a launch's grid rows
+
+// The buffers of one call, checked as they are listed.
+struct Buffers {
+  std::vector<Span> outs, ins;
+  int rc = FSDP_OK;
+
+  void add(std::vector<Span>& to, const void* p, int64_t count, int64_t bytes, uint64_t align, const char* what,
+           long idx) {
+    if (rc) return;
+    int64_t n;
+    if (!mul_ok(count, bytes, &n))
+      rc = fail(FSDP_EINVAL, "%s: size overflow", what);
+    else if (!(rc = check_ptr(p, n, align, what, idx)))
+      to.push_back({(uint64_t)p, (uint64_t)p + (uint64_t)n, (int)(outs.size() + ins.size())});
+  }
+  void out(const void* p, int64_t count, int64_t bytes, const char* what, long idx = 0) {
+    add(outs, p, count, bytes, (uint64_t)bytes, what, idx);
+  }
+  void in(const void* p, int64_t count, int64_t bytes, const char* what, long idx = 0) {
+    add(ins, p, count, bytes, (uint64_t)bytes, what, idx);
+  }
+  int check() const { return rc ? rc : check_overlap(outs, ins); }
+};
+
+int check_count(int64_t v, int64_t least, const char* what) {
+  if (v < least || v >= kMaxRows)
+    return fail(FSDP_EINVAL, "%s %lld outside [%lld, 2^31)", what, (long long)v, (long long)least);
+  return FSDP_OK;
+}
+
+int check_dtype(int32_t dtype, const char* what) {
+  return elem_size(dtype) ? FSDP_OK : fail(FSDP_ENOTIMPL, "%s %d is not supported", what, dtype);
+}
+
+int check_ranks(int32_t n) {
+  if (n < 1 || n > kMaxRanks) return fail(FSDP_EINVAL, "n_ranks %d outside [1, %d]", n, kMaxRanks);
+  return FSDP_OK;
+}
+
+// The dropout of a call: *factor is 1 / (1 - p) for p rounded to a multiple
+// of 2^-16.  rows: the call's rows, each a 32-bit counter of the generator.
+int make_drop(const fsdp_dropout_t* d, int64_t rows, Buffers* b, fsdp::Drop* out, double* factor) {
+  *out = fsdp::Drop{nullptr, 0, 0};
+  *factor = 1.0;
+  if (!d) return FSDP_OK;
+  if (!(d->p >= 0.0 && d->p < 1.0)) return fail(FSDP_EINVAL, "dropout p %g outside [0, 1)", d->p);
+  const uint32_t cut = (uint32_t)(d->p * 65536.0 + 0.5);
+  if (cut >= 65536) return fail(FSDP_EINVAL, "dropout p %g rounds to 1 (p is a multiple of 2^-16)", d->p);
+  if (cut == 0) return FSDP_OK;  // keeps everything
+  if (rows > (int64_t(1) << 32)) return fail(FSDP_EINVAL, "dropout over %lld rows (at most 2^32)", (long long)rows);
+  b->in(d->state, 2, 8, "dropout state");
+  *out = fsdp::Drop{static_cast<const uint64_t*>(d->state), cut, d->site};
+  *factor = 65536.0 / (65536.0 - cut);
+  return FSDP_OK;
+}
+
+// The events of a pending timing request, unless the launch goes into a capture.
+struct Timing {
+  void* start = nullptr;
+  void* stop = nullptr;
+  explicit Timing(void* stream) {
+    if (g_time_start && !capturing(static_cast<hipStream_t>(stream))) {
+      start = g_time_start;
+      stop = g_time_stop;
+      g_time_start = g_time_stop = nullptr;
+    }
+  }
+};
+
+int launched(int he, const char* what) {
+  if (he != hipSuccess) return fail(FSDP_EHIP, "%s launch: %s", what, hipGetErrorString((hipError_t)he));
+  return ok();
+}
+
+// --- embedding ------------------------------------------------------------------
+
+int embedding_impl(int64_t vocab, int64_t cols, int32_t table_dtype, int32_t out_dtype, const void* table,
+                   int64_t n_tokens, int32_t token_bytes, const void* tokens, float scale,
+                   const fsdp_dropout_t* dropout, void* out, void* stream) {
+  int rc;
+  if ((rc = check_count(vocab, 0, "vocab")) || (rc = check_count(cols, 0, "cols")) ||
+      (rc = check_count(n_tokens, 0, "n_tokens")) || (rc = check_dtype(table_dtype, "table dtype")) ||
+      (rc = check_dtype(out_dtype, "output dtype")))
+    return rc;
+  if (token_bytes != 4 && token_bytes != 8) return fail(FSDP_EINVAL, "token_bytes %d not in {4, 8}", token_bytes);
+  Buffers b;
+  b.in(table, vocab * cols, elem_size(table_dtype), "table");
+  b.in(tokens, n_tokens, token_bytes, "tokens");
+  b.out(out, n_tokens * cols, elem_size(out_dtype), "out");
+  fsdp::EmbedArgs a;
+  double keep;
+  if ((rc = make_drop(dropout, n_tokens, &b, &a.drop, &keep)) || (rc = b.check())) return rc;
+  if (n_tokens == 0 || cols == 0) return ok();
+  if (!fsdp::embedding_fits(n_tokens, cols)) return fail(FSDP_EINVAL, "n_tokens * cols too large for one call");
+  a.table = table;
+  a.tokens = tokens;
+  a.out = out;
+  a.n_tokens = n_tokens;
+  a.vocab = vocab;
+  a.cols = cols;
+  a.factor = (float)(scale * keep);
+  a.table_dtype = table_dtype;
+  a.out_dtype = out_dtype;
+  a.token_bytes = token_bytes;
+  const Timing t(stream);
+  return launched(fsdp_launch_embedding(a, stream, t.start, t.stop), "embedding");
+}
+
+// Byte offsets of the gradient's workspace blocks.
+struct GradWorkspace {
+  int64_t order_at, part_at, bytes;
+};
+
+int grad_workspace(int32_t n_ranks, int64_t n_tokens, int64_t vocab, int64_t cols, GradWorkspace* w) {
+  int rc;
+  if ((rc = check_ranks(n_ranks)) || (rc = check_count(vocab, 0, "vocab")) || (rc = check_count(cols, 0, "cols")) ||
+      (rc = check_count(n_tokens, 0, "n_tokens")))
+    return rc;
+  const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+  const int64_t pieces = n_tokens > fsdp::kLong ? (n_tokens + fsdp::kPiece - 1) / fsdp::kPiece : 0;
+  int64_t part;
+  w->order_at = up(4 * (vocab + 1) * n_ranks);
+  w->part_at = w->order_at + up(4 * n_tokens * n_ranks);
+  if (!mul_ok(pieces * 8, cols, &part) || !mul_ok(part, n_ranks, &part) || !add_ok(w->part_at, part, &w->bytes))
+    return fail(FSDP_EINVAL, "workspace size overflow");
+  return FSDP_OK;
+}
+
+int embedding_grad_workspace_impl(int32_t n_ranks, int64_t n_tokens, int64_t vocab, int64_t cols, int64_t* bytes) {
+  GradWorkspace w;
+  const int rc = grad_workspace(n_ranks, n_tokens, vocab, cols, &w);
+  if (rc) return rc;
+  if (bytes) *bytes = w.bytes;
+  return ok();
+}
+
+int check_workspace(const void* p, int64_t have, int64_t need) {
+  if (have < need) return fail(FSDP_EINVAL, "workspace of %lld bytes, %lld needed", (long long)have, (long long)need);
+  if (!p) return fail(FSDP_EINVAL, "workspace is NULL");
+  if ((uint64_t)p % 16) return fail(FSDP_EALIGN, "workspace = %p is not 16-byte aligned", p);
+  return FSDP_OK;
+}
+
+int embedding_grad_impl(int32_t n_ranks, int64_t vocab, int64_t cols, int32_t dtype, int32_t grad_dtype,
+                        int64_t n_tokens, int32_t token_bytes, const void* tokens, const void* dout, float scale,
+                        const fsdp_dropout_t* dropout, int32_t accumulate, void* const* grads, void* workspace,
+                        int64_t workspace_bytes, void* stream) {
+  GradWorkspace w;
+  int rc = grad_workspace(n_ranks, n_tokens, vocab, cols, &w);
+  if (rc || (rc = check_dtype(dtype, "dtype")) || (rc = check_dtype(grad_dtype, "gradient dtype"))) return rc;
+  if (token_bytes != 4 && token_bytes != 8) return fail(FSDP_EINVAL, "token_bytes %d not in {4, 8}", token_bytes);
+  if (!grads) return fail(FSDP_EINVAL, "grads array is NULL");
+  if ((rc = check_workspace(workspace, workspace_bytes, w.bytes))) return rc;
+  int64_t rows, dout_numel;
+  if (!mul_ok(n_tokens, n_ranks, &rows) || !mul_ok(rows, cols, &dout_numel))
+    return fail(FSDP_EINVAL, "dout: size overflow");
+  Buffers b;
+  b.in(tokens, rows, token_bytes, "tokens");
+  b.in(dout, dout_numel, elem_size(dtype), "dout");
+  for (int32_t g = 0; g < n_ranks; ++g) b.out(grads[g], vocab * cols, elem_size(grad_dtype), "grads", g);
+  b.add(b.outs, workspace, w.bytes, 1, 16, "workspace", 0);
+  fsdp::EmbedGradArgs a;
+  double keep;
+  if ((rc = make_drop(dropout, rows, &b, &a.drop, &keep)) || (rc = b.check())) return rc;
+  if (vocab == 0 || cols == 0 || (accumulate && n_tokens == 0)) return ok();
+  if (!fsdp::embedding_grad_fits(n_tokens, vocab, cols))
+    return fail(FSDP_EINVAL, "vocab * cols or n_tokens * cols too large for one call");
+  a.tokens = tokens;
+  a.dout = dout;
+  a.grads = grads;
+  a.off = static_cast<uint32_t*>(workspace);
+  a.order = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + w.order_at);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.part_at);
+  a.n_tokens = n_tokens;
+  a.vocab = vocab;
+  a.cols = cols;
+  a.factor = (float)(scale * keep);
+  a.n_ranks = n_ranks;
+  a.dtype = dtype;
+  a.grad_dtype = grad_dtype;
+  a.token_bytes = token_bytes;
+  a.accumulate = accumulate != 0;
+  const Timing t(stream);
+  return launched(fsdp_launch_embedding_grad(a, stream, t.start, t.stop), "embedding_grad");
+}
+
+// --- norm -----------------------------------------------------------------------
+
+int check_kind(int32_t kind) {
+  if (kind != FSDP_LAYER_NORM && kind != FSDP_RMS_NORM) return fail(FSDP_EINVAL, "norm kind %d", kind);
+  return FSDP_OK;
+}
+
+int norm_impl(int32_t kind, int64_t rows, int64_t cols, int32_t dtype, int32_t weight_dtype, const void* x,
+              const void* residual, const fsdp_dropout_t* dropout, const void* weight, const void* bias, float eps,
+              void* h, void* y, float* mean, float* rstd, void* stream) {
+  int rc;
+  if ((rc = check_kind(kind)) || (rc = check_count(rows, 0, "rows")) || (rc = check_count(cols, 1, "cols")) ||
+      (rc = check_dtype(dtype, "dtype")) || (rc = check_dtype(weight_dtype, "weight dtype")))
+    return rc;
+  if (!(eps >= 0.0f) || std::isinf(eps)) return fail(FSDP_EINVAL, "eps %g", eps);
+  const int es = elem_size(dtype), ws = elem_size(weight_dtype);
+  Buffers b;
+  b.in(x, rows * cols, es, "x");
+  if (residual) b.in(residual, rows * cols, es, "residual");
+  b.in(weight, cols, ws, "weight");
+  if (bias) b.in(bias, cols, ws, "bias");
+  if (h) b.out(h, rows * cols, es, "h");
+  b.out(y, rows * cols, es, "y");
+  if (mean) b.out(mean, rows, 4, "mean");
+  if (rstd) b.out(rstd, rows, 4, "rstd");
+  fsdp::NormArgs a;
+  double keep;
+  if ((rc = make_drop(dropout, rows, &b, &a.drop, &keep)) || (rc = b.check())) return rc;
+  if (!h && rows > 0 && (residual || a.drop.state))
+    return fail(FSDP_EINVAL, "h is NULL: a residual or a dropout needs it (the gradient reads it)");
+  if (rows == 0) return ok();
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.bias = bias;
+  a.h = h;
+  a.y = y;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.rows = rows;
+  a.cols = cols;
+  a.eps = eps;
+  a.factor = (float)keep;
+  a.rms = kind == FSDP_RMS_NORM;
+  a.dtype = dtype;
+  a.weight_dtype = weight_dtype;
+  const Timing t(stream);
+  return launched(fsdp_launch_norm(a, stream, t.start, t.stop), "norm");
+}
+
+int norm_workspace(int32_t n_ranks, int64_t rows, int64_t cols, int* blocks, int64_t* bytes) {
+  int rc;
+  if ((rc = check_ranks(n_ranks)) || (rc = check_count(rows, 0, "rows")) || (rc = check_count(cols, 1, "cols")))
+    return rc;
+  *blocks = fsdp::norm_grad_blocks(rows, cols, n_ranks);
+  if (!mul_ok((int64_t)*blocks * n_ranks * 8, cols, bytes)) return fail(FSDP_EINVAL, "workspace size overflow");
+  return FSDP_OK;
+}
+
+int norm_grad_workspace_impl(int32_t n_ranks, int64_t rows, int64_t cols, int64_t* bytes) {
+  int blocks;
+  int64_t n;
+  const int rc = norm_workspace(n_ranks, rows, cols, &blocks, &n);
+  if (rc) return rc;
+  if (bytes) *bytes = n;
+  return ok();
+}
+
+int norm_grad_impl(int32_t kind, int32_t n_ranks, int64_t rows, int64_t cols, int32_t dtype, int32_t weight_dtype,
+                   int32_t grad_dtype, const void* dy, const void* dh, const void* h, const float* mean,
+                   const float* rstd, const void* weight, const fsdp_dropout_t* dropout, int32_t accumulate,
+                   void* dres, void* dx, void* const* dweight, void* const* dbias, void* workspace,
+                   int64_t workspace_bytes, void* stream) {
+  fsdp::NormGradArgs a;
+  int64_t need, n, numel;
+  int rc = norm_workspace(n_ranks, rows, cols, &a.blocks, &need);
+  if (rc || (rc = check_kind(kind)) || (rc = check_dtype(dtype, "dtype")) ||
+      (rc = check_dtype(weight_dtype, "weight dtype")) || (rc = check_dtype(grad_dtype, "gradient dtype")))
+    return rc;
+  if (!dweight) return fail(FSDP_EINVAL, "dweight array is NULL");
+  if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
+  if (!mul_ok(rows, n_ranks, &n) || !mul_ok(n, cols, &numel)) return fail(FSDP_EINVAL, "dy: size overflow");
+  const int es = elem_size(dtype), gs = elem_size(grad_dtype);
+  Buffers b;
+  b.in(dy, numel, es, "dy");
+  if (dh) b.in(dh, numel, es, "dh");
+  b.in(h, numel, es, "h");
+  if (kind == FSDP_LAYER_NORM) b.in(mean, n, 4, "mean");
+  b.in(rstd, n, 4, "rstd");
+  b.in(weight, cols, elem_size(weight_dtype), "weight");
+  b.out(dres, numel, es, "dres");
+  if (dx) b.out(dx, numel, es, "dx");
+  for (int32_t g = 0; g < n_ranks; ++g) {
+    b.out(dweight[g], cols, gs, "dweight", g);
+    if (dbias) b.out(dbias[g], cols, gs, "dbias", g);
+  }
+  b.add(b.outs, workspace, need, 1, 16, "workspace", 0);
+  double keep;
+  if ((rc = make_drop(dropout, n, &b, &a.drop, &keep)) || (rc = b.check())) return rc;
+  if (a.drop.state && !dx && n > 0) return fail(FSDP_EINVAL, "dx is NULL: with a dropout it differs from dres");
+  if (accumulate && rows == 0) return ok();
+  a.dy = dy;
+  a.dh = dh;
+  a.h = h;
+  a.mean = kind == FSDP_LAYER_NORM ? mean : nullptr;
+  a.rstd = rstd;
+  a.weight = weight;
+  a.dres = dres;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.part = static_cast<float*>(workspace);
+  a.rows = rows;
+  a.cols = cols;
+  a.factor = (float)keep;
+  a.n_ranks = n_ranks;
+  a.rms = kind == FSDP_RMS_NORM;
+  a.dtype = dtype;
+  a.weight_dtype = weight_dtype;
+  a.grad_dtype = grad_dtype;
+  a.accumulate = accumulate != 0;
+  const Timing t(stream);
+  return launched(fsdp_launch_norm_grad(a, stream, t.start, t.stop), "norm_grad");
+}
+
+}  // namespace
+
+extern "C" {
+
+int fsdp_embedding(int64_t vocab, int64_t cols, int32_t table_dtype, int32_t out_dtype, const void* table,
+                   int64_t n_tokens, int32_t token_bytes, const void* tokens, float scale,
+                   const fsdp_dropout_t* dropout, void* out, void* stream) {
+  return guarded([&] {
+    return embedding_impl(vocab, cols, table_dtype, out_dtype, table, n_tokens, token_bytes, tokens, scale, dropout,
+                          out, stream);
+  });
+}
+
+int fsdp_embedding_grad_workspace(int32_t n_ranks, int64_t n_tokens, int64_t vocab, int64_t cols, int64_t* bytes) {
+  return guarded([&] { return embedding_grad_workspace_impl(n_ranks, n_tokens, vocab, cols, bytes); });
+}
+
+int fsdp_embedding_grad(int32_t n_ranks, int64_t vocab, int64_t cols, int32_t dtype, int32_t grad_dtype,
+                        int64_t n_tokens, int32_t token_bytes, const void* tokens, const void* dout, float scale,
+                        const fsdp_dropout_t* dropout, int32_t accumulate, void* const* grads, void* workspace,
+                        int64_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    return embedding_grad_impl(n_ranks, vocab, cols, dtype, grad_dtype, n_tokens, token_bytes, tokens, dout, scale,
+                               dropout, accumulate, grads, workspace, workspace_bytes, stream);
+  });
+}
+
+int fsdp_norm(int32_t kind, int64_t rows, int64_t cols, int32_t dtype, int32_t weight_dtype, const void* x,
+              const void* residual, const fsdp_dropout_t* dropout, const void* weight, const void* bias, float eps,
+              void* h, void* y, float* mean, float* rstd, void* stream) {
+  return guarded([&] {
+    return norm_impl(kind, rows, cols, dtype, weight_dtype, x, residual, dropout, weight, bias, eps, h, y, mean, rstd,
+                     stream);
+  });
+}
+
+int fsdp_norm_grad_workspace(int32_t n_ranks, int64_t rows, int64_t cols, int64_t* bytes) {
+  return guarded([&] { return norm_grad_workspace_impl(n_ranks, rows, cols, bytes); });
+}
+
+int fsdp_norm_grad(int32_t kind, int32_t n_ranks, int64_t rows, int64_t cols, int32_t dtype, int32_t weight_dtype,
+                   int32_t grad_dtype, const void* dy, const void* dh, const void* h, const float* mean,
+                   const float* rstd, const void* weight, const fsdp_dropout_t* dropout, int32_t accumulate,
+                   void* dres, void* dx, void* const* dweight, void* const* dbias, void* workspace,
+                   int64_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    return norm_grad_impl(kind, n_ranks, rows, cols, dtype, weight_dtype, grad_dtype, dy, dh, h, mean, rstd, weight,
+                          dropout, accumulate, dres, dx, dweight, dbias, workspace, workspace_bytes, stream);
+  });
+}
+
+}  // extern "C"

@@ -3,8 +3,8 @@
  *
  * One bucket of P parameters, sharded (on dim 0 unless a parameter states
  * another dim) over a shard group of S ranks and replicated over D = R / S
- * replicate groups, R simulated ranks resident in one GPU's HBM.  Every device entry point is one HIP kernel launch,
- * enqueued on the caller's stream.  A call whose descriptor table (a
+ * replicate groups, R simulated ranks resident in one GPU's HBM.  Every device entry point of that path is one HIP kernel
+ * launch, enqueued on the caller's stream.  A call whose descriptor table (a
  * function of its shapes, sizes and pointers) is new uploads that table
  * once with a blocking copy; a repeated call makes no HIP call besides the
  * launch and does not synchronise the host.
@@ -49,7 +49,8 @@
  *     fsdp_fused_ar, which works in place by definition.
  *   - Padding is written as zero on every call; no output needs to be
  *     cleared beforehand.
- *   - The library caches a plan per call signature (entry point, sizes,
+ *   - The library caches a plan per call signature of the flat-buffer entry
+ *     points (the token operators have none; entry point, sizes,
  *     shapes, shard dims, pointers, device): the call's descriptor table in
  *     device memory and its launch parameters.  A repeated call launches its
  *     plan without validating or planning again (its result cannot differ).
@@ -266,6 +267,128 @@ int fsdp_rs_copy_reduce_noalloc(const fsdp_bucket_t* bucket, int32_t rank_size, 
 int fsdp_fused_ar(int32_t n_seg, const int64_t* seg_numel, int32_t rank_size,
                   int32_t shard_size, int32_t dp_size, int32_t op, int32_t dtype,
                   void* const* fused, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Token operators (async on `stream`)
+ *
+ * What a layer does between the full parameters that the AllGather delivers
+ * and the full gradients that the ReduceScatter takes, apart from its matrix
+ * products: the embedding lookup, and the norm behind a residual add, each
+ * with its gradient.  They read a parameter where AG copy-out put it (or, for
+ * a one-parameter bucket sharded on dim 0, at the start of the gathered
+ * buffer, which needs no copy-out) and write its gradient where RS copy-in or
+ * the fused RS copy-reduce reads it (or at the start of that bucket's RS
+ * inputs).
+ *
+ *   - Activations are dense rows of `cols` elements.  The R ranks' rows stand
+ *     one rank after the other; a gradient entry point takes all n_ranks of
+ *     them in one call and writes one parameter gradient per rank.  With one
+ *     process per GPU n_ranks is 1.
+ *   - Elements are FSDP_F32, FSDP_BF16 or FSDP_F16, activations, parameters
+ *     and gradients each of its own type.  Every sum, mean and variance is
+ *     fp32; every output is rounded once, to nearest even.
+ *   - Rows, columns, tokens (of one rank) and vocabulary are below 2^31.
+ *     Rows need only their element's alignment, whatever `cols` is.
+ *   - Sums have a fixed order, a function of the sizes and tokens alone: the
+ *     same call gives the same bits.
+ *   - No call allocates, uploads or caches anything: each one is a fixed
+ *     sequence of kernel launches, so any call can be captured into a HIP
+ *     graph, its first one included.  The gradients' workspaces belong to the
+ *     caller and hold nothing between calls; calls that overlap in time (two
+ *     streams, two graphs replayed at once) need workspaces of their own.
+ *   - accumulate = 0 writes a gradient entirely (rows without a token as
+ *     zeros); accumulate != 0 adds to it in fp32 and rounds once.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Dropout behind the lookup or before the residual add; NULL or p = 0: none.
+ * Element e of row t is dropped where lane e % 8 (16 bits, lowest first) of
+ * Philox4x32-7 (Salmon, Moraes, Dror, Shaw, SC 2011) at counter (e / 8, t,
+ * site, step mod 2^32) and key seed is below cut = round(65536 p); a kept one
+ * is scaled by 65536 / (65536 - cut), a dropped one is +0 whatever it was.  No
+ * mask is stored: a gradient given the same p, site, seed and step draws it
+ * again.  t counts the call's rows over all ranks.
+ *   p      in [0, 1), used as a multiple of 2^-16; one that rounds to 1 is
+ *          FSDP_EINVAL
+ *   site   tells the dropouts of one step apart
+ *   state  device pointer to two 64-bit words, seed and step, read by the
+ *          kernels: advance step between training steps (a captured graph
+ *          then draws another mask on each replay)
+ */
+typedef struct fsdp_dropout {
+  double p;
+  uint32_t site;
+  const void* state;
+} fsdp_dropout_t;
+
+/* kinds of norm */
+#define FSDP_LAYER_NORM 0  /* (h - mean) / sqrt(var + eps) */
+#define FSDP_RMS_NORM   1  /* h / sqrt(mean(h^2) + eps)    */
+
+/*
+ * out[t] = drop(scale * table[tokens[t]]).  A token outside [0, vocab) (a
+ * padding token, another shard's) gives a row of zeros; the table is not read
+ * for it.
+ *   table   vocab x cols of table_dtype
+ *   tokens  n_tokens integers of token_bytes (4 or 8) each, signed
+ *   out     n_tokens x cols of out_dtype
+ */
+int fsdp_embedding(int64_t vocab, int64_t cols, int32_t table_dtype, int32_t out_dtype, const void* table,
+                   int64_t n_tokens, int32_t token_bytes, const void* tokens, float scale,
+                   const fsdp_dropout_t* dropout, void* out, void* stream);
+
+/*
+ * grads[g][v] = scale * sum of drop'(dout[t]) over rank g's rows t with token
+ * v, in ascending t for a token of up to 64 rows, else ascending within runs
+ * of 64 whose sums are then added; drop' zeroes and scales as the lookup's
+ * dropout did.  Tokens outside [0, vocab) add nothing.  With accumulate, rows
+ * of grads without a token are neither read nor written.
+ *   tokens     [n_ranks][n_tokens];  dout: [n_ranks * n_tokens] x cols of dtype
+ *   grads      [n_ranks] device pointers (a host array), each vocab x cols of
+ *              grad_dtype
+ *   workspace  fsdp_embedding_grad_workspace bytes, 16-byte aligned
+ */
+int fsdp_embedding_grad_workspace(int32_t n_ranks, int64_t n_tokens, int64_t vocab, int64_t cols, int64_t* bytes);
+int fsdp_embedding_grad(int32_t n_ranks, int64_t vocab, int64_t cols, int32_t dtype, int32_t grad_dtype,
+                        int64_t n_tokens, int32_t token_bytes, const void* tokens, const void* dout, float scale,
+                        const fsdp_dropout_t* dropout, int32_t accumulate, void* const* grads, void* workspace,
+                        int64_t workspace_bytes, void* stream);
+
+/*
+ * Over the last dim of every row:
+ *   h = residual + drop(x), rounded to dtype (h = x without either)
+ *   y = (h - mean) * rstd * weight + bias,  rstd = 1 / sqrt(var + eps)
+ * (FSDP_RMS_NORM: mean 0, var = mean(h^2)).  The norm is of the rounded h,
+ * which is what its gradient reads.
+ *   x, residual, h, y  rows x cols of dtype; residual may be NULL; h may be
+ *                      NULL when there is neither residual nor dropout
+ *   weight, bias       cols of weight_dtype; bias may be NULL
+ *   mean, rstd         rows floats each for the gradient; either may be NULL
+ */
+int fsdp_norm(int32_t kind, int64_t rows, int64_t cols, int32_t dtype, int32_t weight_dtype, const void* x,
+              const void* residual, const fsdp_dropout_t* dropout, const void* weight, const void* bias, float eps,
+              void* h, void* y, float* mean, float* rstd, void* stream);
+
+/*
+ * With xhat = (h - mean) * rstd and g = dy * weight, row by row:
+ *   dres = rstd * (g - mean(g) - xhat * mean(g * xhat)) + dh
+ *   dx   = drop'(dres)
+ * (FSDP_RMS_NORM: without mean(g)), and over rank r's rows
+ *   dweight[r] = sum dy * xhat,  dbias[r] = sum dy.
+ * dres is the gradient of h, so also of the residual; dx that of x.  dh is
+ * what reaches h past the norm, through the residual stream.
+ *   rows           of one rank: every row buffer has n_ranks * rows of them
+ *   dh, dx, dbias  may be NULL (dx not with a dropout)
+ *   mean           read for FSDP_LAYER_NORM only
+ *   dweight, dbias [n_ranks] device pointers (host arrays), cols of grad_dtype
+ *   workspace      fsdp_norm_grad_workspace bytes, 16-byte aligned
+ */
+int fsdp_norm_grad_workspace(int32_t n_ranks, int64_t rows, int64_t cols, int64_t* bytes);
+int fsdp_norm_grad(int32_t kind, int32_t n_ranks, int64_t rows, int64_t cols, int32_t dtype, int32_t weight_dtype,
+                   int32_t grad_dtype, const void* dy, const void* dh, const void* h, const float* mean,
+                   const float* rstd, const void* weight, const fsdp_dropout_t* dropout, int32_t accumulate,
+                   void* dres, void* dx, void* const* dweight, void* const* dbias, void* workspace,
+                   int64_t workspace_bytes, void* stream);
 
 /* Message for the calling thread's last error ("" after success). */
 const char* fsdp_last_error(void);

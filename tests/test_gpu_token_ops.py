@@ -1,0 +1,658 @@
+"""Token operators on the GPU against the float64 oracle.
+
+Tolerances, element by element, from the kernels' arithmetic (U = 2^-24, half
+an fp32 step; H = half a step of the output's type, relative; TINY its smallest
+step, for results among the denormals):
+  embedding       the factor and the product are rounded, then the output:
+                  (H + 2 U) |out|
+  embedding_grad  n terms are added in fp32, then scaled and rounded (and added
+                  to the old value): (n + 4) U sum|terms| + H |result|
+  norm            K bounds the additions on the longest path of a row's sums
+                  (a lane's own columns, then the tree over the lanes).  The
+                  mean is off by at most K U mean|d|, d = h - mean, its square
+                  sum relatively by (K + 4) U; mean|d| <= 1 / rstd
+  norm_grad       the same for mean(g) and mean(g xhat); dweight and dbias like
+                  embedding_grad's sums over the rank's rows
+Buffers are NaN-filled, guarded on both sides and start at odd elements, so
+that no row is aligned by chance.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import Guarded, bits, note, require_gpu
+from oracle import token_oracle as T
+
+hp = pytest.importorskip("hsdp_parameter_gradient_amd")
+
+pytestmark = pytest.mark.gpu
+
+TYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+TINY = {"f32": 2.0 ** -149, "bf16": 2.0 ** -133, "f16": 2.0 ** -24}
+U = 2.0 ** -24
+SEED, STEP, SITE = 0x1234_5678_9ABC_DEF, 41, 7
+
+
+def _rng(*key):
+    return np.random.default_rng(list(key))
+
+
+def _values(rng, shape, name, sigma=1.0, mean=0.0):
+    """Random values of a type, as float64."""
+    return T.round_to(mean + sigma * rng.standard_normal(shape), name)
+
+
+def _dev(a, name, offset=0):
+    """A guarded device copy of float64 values of a type."""
+    g = Guarded(a.size, TYPE[name], offset)
+    g.t.copy_(torch.from_numpy(np.ascontiguousarray(a).reshape(-1)).to(TYPE[name]))
+    g.view = g.t.view(a.shape)
+    return g
+
+
+def _out(shape, name, offset=0):
+    g = Guarded(int(np.prod(shape)), TYPE[name], offset)
+    g.view = g.t.view(shape)
+    return g
+
+
+def _host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _close(what, got, want, tol):
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), "%s: %d of %d off, first at %s: got %r want %r tol %r" % (
+        what, bad.sum(), bad.size, np.argwhere(bad)[0], got[bad][0], want[bad][0],
+        np.broadcast_to(tol, got.shape)[bad][0])
+
+
+def _state(seed=SEED, step=STEP):
+    return torch.tensor([seed, step], dtype=torch.int64, device="cuda")
+
+
+def _drop(p, state=None):
+    return hp.Dropout(p, _state() if state is None else state, SITE) if p else None
+
+
+def _factors(rows, cols, p):
+    return T.dropout_factors(rows, cols, p, SEED, STEP, SITE) if p else None
+
+
+def _tokens(rng, n, vocab, kind):
+    if kind == "spread":
+        return rng.integers(0, vocab, n)
+    if kind == "skewed":  # most positions on few tokens, some on none
+        return np.minimum((vocab * rng.random(n) ** 6).astype(np.int64), vocab - 1)
+    if kind == "one":
+        return np.full(n, vocab - 1)
+    if kind == "padded":
+        t = rng.integers(0, vocab, n)
+        t[rng.random(n) < 0.5] = -1
+        return t
+    assert kind == "outside"
+    t = rng.integers(-2, vocab + 3, n)
+    if n > 2:
+        t[0], t[1] = -(2 ** 31), 2 ** 31 - 1
+    return t
+
+
+# --- embedding ------------------------------------------------------------------
+
+EMBED = [  # tokens, vocab, cols, table, out, scale, p, tokens' kind, token type
+    (1, 1, 1, "f32", "f32", 1.0, 0.0, "spread", torch.int64),
+    (5, 7, 8, "bf16", "bf16", 1.0, 0.0, "outside", torch.int64),
+    (64, 100, 64, "f16", "f16", 1.0, 0.0, "spread", torch.int32),
+    (33, 50, 7, "f32", "bf16", 0.5, 0.0, "padded", torch.int64),
+    (130, 1300, 129, "bf16", "f32", 3.7, 0.1, "skewed", torch.int32),
+    (17, 300, 1023, "f16", "bf16", 8.0, 0.5, "spread", torch.int64),
+    (9, 40, 4096, "bf16", "bf16", 64.0, 0.25, "outside", torch.int64),
+    (3, 5, 8197, "f32", "f16", 1.0, 0.1, "spread", torch.int32),
+    (2, 3, 262152, "bf16", "bf16", 1.0, 0.0, "spread", torch.int64),
+    (3, 3, 300001, "bf16", "f16", 1.5, 0.0, "spread", torch.int64),
+    (2049, 11, 24, "f16", "f32", 1.0, 0.0, "padded", torch.int64),
+]
+
+
+@pytest.mark.parametrize("case", EMBED, ids=lambda c: "-".join(str(v) for v in c))
+def test_embedding(case):
+    require_gpu()
+    n, V, E, td, od, scale, p, kind, ttype = case
+    note(f"[embedding] {case}")
+    rng = _rng(1, n, V, E)
+    tok, table = _tokens(rng, n, V, kind), _values(rng, (V, E), td, 2.0)
+    dt, tt, out = _dev(table, td, 1), torch.from_numpy(tok).to(ttype).cuda(), _out((n, E), od, 3)
+    hp.fsdp_embedding(tt, dt.view, out.view, scale=scale, dropout=_drop(p))
+    torch.cuda.synchronize()
+    assert out.guards_intact() and dt.guards_intact()
+    want = T.embedding(tok, table, scale, _factors(n, E, p))
+    if td == od and scale == 1.0 and not p:
+        assert np.array_equal(_host(out.view), want)
+    else:
+        _close("out", _host(out.view), want, (HALF[od] + 2 * U) * 1.01 * np.abs(want) + TINY[od])
+
+
+EGRAD = [  # ranks, tokens, vocab, cols, dout, grad, scale, p, kind, accumulate, token type
+    (1, 1, 1, 1, "f32", "f32", 1.0, 0.0, "spread", False, torch.int64),
+    (1, 0, 5, 6, "bf16", "f32", 1.0, 0.0, "spread", False, torch.int64),
+    (2, 3, 7, 8, "bf16", "f32", 1.0, 0.0, "outside", False, torch.int64),
+    (1, 64, 511, 4, "f16", "f16", 2.0, 0.0, "one", False, torch.int32),
+    (1, 65, 512, 5, "f16", "f32", 2.0, 0.0, "one", False, torch.int64),
+    (3, 65, 513, 7, "f32", "f32", 1.0, 0.25, "skewed", False, torch.int32),
+    (2, 130, 513, 12, "bf16", "bf16", 1.0, 0.0, "one", True, torch.int64),
+    (1, 1000, 1300, 33, "bf16", "f32", 0.5, 0.0, "skewed", True, torch.int64),
+    (2, 1000, 40, 100, "f32", "f32", 1.0, 0.1, "spread", False, torch.int64),
+    (1, 700, 3, 131, "bf16", "f32", 1.0, 0.0, "spread", False, torch.int64),
+    (2, 129, 2000, 1025, "bf16", "f32", 45.25, 0.1, "padded", False, torch.int64),
+    (1, 4097, 5, 21, "f16", "f32", 1.0, 0.0, "skewed", False, torch.int64),
+    (70, 9, 6, 10, "f32", "f32", 1.0, 0.0, "outside", False, torch.int64),
+    (70, 70, 2, 10, "f32", "bf16", 1.0, 0.0, "one", True, torch.int32),
+    (1, 2500, 9, 600, "bf16", "f32", 1.0, 0.5, "one", True, torch.int64),
+]
+
+
+@pytest.mark.parametrize("case", EGRAD, ids=lambda c: "-".join(str(v) for v in c))
+def test_embedding_grad(case):
+    require_gpu()
+    R, n, V, E, dd, gd, scale, p, kind, add, ttype = case
+    note(f"[embedding_grad] {case}")
+    rng = _rng(2, R, n, V, E)
+    tok = np.stack([_tokens(rng, n, V, kind) for _ in range(R)])
+    dout = _values(rng, (R * n, E), dd)
+    old = _values(rng, (R, V, E), gd, 3.0)
+    d, tt = _dev(dout, dd, 3), torch.from_numpy(tok).to(ttype).cuda()
+    grads = [_dev(old[g], gd, 1) if add else _out((V, E), gd, 1) for g in range(R)]
+    hp.fsdp_embedding_grad(tt, d.view, [g.view for g in grads], scale=scale, dropout=_drop(p), accumulate=add)
+    first = [bits(g.view) for g in grads]
+    if not add:  # the same bits again
+        hp.fsdp_embedding_grad(tt, d.view, [g.view for g in grads], scale=scale, dropout=_drop(p))
+        assert all(np.array_equal(a, bits(g.view)) for a, g in zip(first, grads))
+    torch.cuda.synchronize()
+    f = _factors(R * n, E, p)
+    for g in range(R):
+        assert grads[g].guards_intact()
+        at = slice(g * n, (g + 1) * n)
+        want, size = T.embedding_grad(tok[g], dout[at], V, scale, None if f is None else f[at])
+        count = np.array([(tok[g] == v).sum() for v in range(V)])[:, None]
+        got, tol = _host(grads[g].view), (count + 4) * U * size
+        if add:
+            want, tol = want + old[g], tol + U * np.abs(want + old[g])
+            untouched = count[:, 0] == 0
+            assert np.array_equal(got[untouched], old[g][untouched])
+        _close(f"grad {g}", got, want, (tol + HALF[gd] * np.abs(want)) * 1.01 + TINY[gd])
+
+
+@pytest.mark.parametrize("p", [0.0, 0.3])
+def test_embedding_gradient_is_the_adjoint(p):
+    """The lookup is linear in the table: <dout, embedding(D)> = <grad(dout), D>
+    for any D, which is also the difference quotient of <dout, embedding(t)>
+    along D.  Both sides are sums of n E products, each off by at most 2 U
+    (and the gradient's sums by at most (n + 4) U of their terms)."""
+    require_gpu()
+    note(f"[embedding] adjoint p={p}")
+    rng = _rng(3)
+    n, V, E = 150, 20, 37
+    tok = torch.from_numpy(_tokens(rng, n, V, "outside")).cuda()
+    D, dout = _values(rng, (V, E), "f32"), _values(rng, (n, E), "f32")
+    dD, dd = _dev(D, "f32"), _dev(dout, "f32")
+    out, grad = _out((n, E), "f32"), _out((V, E), "f32")
+    hp.fsdp_embedding(tok, dD.view, out.view, scale=1.7, dropout=_drop(p))
+    hp.fsdp_embedding_grad(tok, dd.view, [grad.view], scale=1.7, dropout=_drop(p))
+    a, b = _host(out.view) * dout, _host(grad.view) * D
+    size = 1.7 / (1 - p) * sum(np.abs(dout[t] * D[v]).sum() for t, v in enumerate(tok.tolist()) if 0 <= v < V)
+    assert abs(a.sum() - b.sum()) <= (n + 8) * U * size
+
+
+# --- norm -----------------------------------------------------------------------
+
+def _depth(cols):
+    """The longest chain of additions of a row's sum."""
+    return 8 * max(2, -(-cols // 8192)) + 6 + 16
+
+
+def _h_tol(x, res, f, act):
+    t = x if f is None else T._times(x, f)
+    h = t if res is None else res + t
+    return h, HALF[act] * np.abs(h) + 2 * U * np.abs(t) + U * np.abs(h) + TINY[act]
+
+
+NORM = [  # rows, cols, act, weight, kind, bias, residual, p, mean of x
+    (1, 1, "f32", "f32", "rms", False, False, 0.0, 0.0),
+    (3, 1, "f32", "f32", "layer", True, False, 0.0, 0.0),
+    (5, 7, "bf16", "bf16", "layer", True, True, 0.0, 0.0),
+    (33, 64, "f16", "f32", "rms", False, True, 0.25, 0.0),
+    (17, 127, "f32", "f32", "layer", True, True, 0.1, 100.0),
+    (17, 128, "bf16", "f32", "layer", False, False, 0.0, 0.0),
+    (20, 129, "bf16", "bf16", "rms", True, True, 0.0, 0.0),
+    (7, 512, "f16", "f16", "layer", True, False, 0.0, 0.0),
+    (6, 513, "f32", "bf16", "layer", True, True, 0.0, 1000.0),
+    (9, 1021, "f32", "f32", "rms", False, True, 0.0, 0.0),
+    (4, 1024, "bf16", "bf16", "layer", True, True, 0.1, 0.0),
+    (5, 1025, "f16", "f32", "layer", False, False, 0.3, 0.0),
+    (5, 2048, "bf16", "bf16", "rms", False, False, 0.0, 0.0),
+    (3, 2056, "bf16", "f32", "layer", True, True, 0.0, 0.0),
+    (3, 4096, "bf16", "bf16", "layer", True, True, 0.1, 0.0),
+    (3, 4097, "f32", "f32", "rms", False, True, 0.0, 0.0),
+    (2, 8192, "f16", "f16", "layer", True, True, 0.0, 0.0),
+    (2, 8195, "bf16", "bf16", "layer", True, False, 0.1, 0.0),
+    (2, 16384, "f32", "f32", "layer", True, True, 0.0, 30.0),
+    (2, 16392, "bf16", "bf16", "layer", True, True, 0.1, 0.0),
+    (3, 20001, "f32", "f32", "rms", False, False, 0.0, 0.0),
+    (3, 40007, "f16", "f32", "layer", True, True, 0.0, 0.0),
+]
+
+
+@pytest.mark.parametrize("case", NORM, ids=lambda c: "-".join(str(v) for v in c))
+def test_norm(case):
+    require_gpu()
+    n, E, act, wd, kind, has_bias, has_res, p, mu = case
+    note(f"[norm] {case}")
+    rng = _rng(4, n, E)
+    x, w = _values(rng, (n, E), act, 1.0, mu), _values(rng, (E,), wd, 0.3, 1.0)
+    b = _values(rng, (E,), wd, 0.3) if has_bias else None
+    res = _values(rng, (n, E), act, 1.0, 0.5) if has_res else None
+    eps, rms = 1e-5, kind == "rms"
+    dx, dw = _dev(x, act, 3), _dev(w, wd, 1)
+    db, dr = (None if v is None else _dev(v, t, 5) for v, t in ((b, wd), (res, act)))
+    h = _out((n, E), act, 1) if has_res or p else None
+    y, mean, rstd = _out((n, E), act, 7), _out((n,), "f32", 1), _out((n,), "f32", 2)
+    hp.fsdp_norm(dx.view, dw.view, y.view, bias=db and db.view, residual=dr and dr.view, h=h and h.view,
+                 mean=mean.view, rstd=rstd.view, eps=eps, kind=kind, dropout=_drop(p))
+    torch.cuda.synchronize()
+    assert all(g.guards_intact() for g in (y, mean, rstd) + ((h,) if h else ()))
+    hv = x
+    if h:
+        want, tol = _h_tol(x, res, _factors(n, E, p), act)
+        hv = _host(h.view)
+        _close("h", hv, want, tol * 1.01)
+    want, m, r = T.norm(hv, w, b, float(np.float32(eps)), rms)
+    K = _depth(E)
+    d = hv - m[:, None]
+    md = np.abs(d).mean(1)
+    _close("mean", _host(mean.view), m, (K * U * md + 2 * U * np.abs(m)) * 1.01)
+    _close("rstd", _host(rstd.view), r, ((K + 4) / 2 + 4) * U * r * 1.01)
+    xw = np.abs(d * r[:, None] * w)
+    tol = K * U * np.abs(w) * (md * r)[:, None] + ((K + 4) / 2 + 10) * U * xw + 3 * U * np.abs(want)
+    if b is not None:
+        tol = tol + U * np.abs(b)
+    _close("y", _host(y.view), want, (tol + HALF[act] * np.abs(want)) * 1.01 + TINY[act])
+
+
+NGRAD = [  # ranks, rows, cols, act, weight, grad, kind, bias, dh, p, accumulate
+    (1, 1, 1, "f32", "f32", "f32", "rms", False, False, 0.0, False),
+    (1, 0, 9, "f32", "f32", "f32", "layer", True, False, 0.0, False),
+    (2, 5, 7, "bf16", "bf16", "f32", "layer", True, True, 0.0, False),
+    (1, 100, 64, "f16", "f32", "f16", "rms", False, True, 0.25, False),
+    (3, 40, 128, "bf16", "f32", "f32", "layer", True, False, 0.0, True),
+    (2, 33, 129, "f32", "f32", "f32", "layer", False, True, 0.0, False),
+    (1, 9, 512, "bf16", "bf16", "bf16", "layer", True, True, 0.1, False),
+    (2, 600, 520, "f32", "f32", "f32", "rms", False, False, 0.0, True),
+    (1, 700, 1021, "f32", "bf16", "f32", "layer", True, True, 0.0, False),
+    (2, 6, 1024, "bf16", "bf16", "f32", "layer", True, True, 0.1, False),
+    (70, 2, 40, "bf16", "bf16", "f32", "layer", True, True, 0.0, False),
+    (1, 5, 1025, "f16", "f16", "f32", "layer", True, False, 0.3, True),
+    (2, 3, 2048, "bf16", "f32", "f32", "rms", False, True, 0.0, False),
+    (1, 600, 2049, "f32", "f32", "f32", "layer", True, False, 0.0, False),
+    (2, 4, 4096, "bf16", "bf16", "f32", "layer", True, True, 0.1, False),
+    (1, 3, 4099, "f32", "f32", "f32", "rms", True, True, 0.0, True),
+    (1, 4, 8192, "bf16", "bf16", "f32", "layer", True, True, 0.0, False),
+    (2, 2, 8193, "bf16", "bf16", "f32", "layer", True, True, 0.1, False),
+    (1, 3, 16385, "f32", "f32", "f32", "layer", True, True, 0.0, True),
+    (1, 3, 30011, "f16", "f32", "bf16", "rms", False, False, 0.0, False),
+]
+
+
+@pytest.mark.parametrize("case", NGRAD, ids=lambda c: "-".join(str(v) for v in c))
+def test_norm_grad(case):
+    require_gpu()
+    R, n, E, act, wd, gd, kind, has_bias, has_dh, p, add = case
+    note(f"[norm_grad] {case}")
+    rng, rms = _rng(5, R, n, E), kind == "rms"
+    h, dy = _values(rng, (R * n, E), act, 1.0, 0.5), _values(rng, (R * n, E), act)
+    w, dh = _values(rng, (E,), wd, 0.3, 1.0), _values(rng, (R * n, E), act) if has_dh else None
+    _, m, r = T.norm(h, w, None, 1e-3, rms)
+    m, r = T.round_to(m, "f32"), T.round_to(r, "f32")
+    old = _values(rng, (2, R, E), gd, 3.0)
+    d = {k: _dev(v, t, o) for k, v, t, o in (("dy", dy, act, 1), ("h", h, act, 3), ("m", m, "f32", 1),
+                                              ("r", r, "f32", 2), ("w", w, wd, 5))}
+    if has_dh:
+        d["dh"] = _dev(dh, act, 7)
+    dres, dx = _out((R * n, E), act, 1), _out((R * n, E), act, 5) if p else None
+    grads = [[_dev(old[s, g], gd, 1 + s) if add else _out((E,), gd, 1 + s) for g in range(R)] for s in range(2)]
+
+    def call():
+        hp.fsdp_norm_grad(d["dy"].view, d["h"].view, d["r"].view, d["w"].view, dres.view, [g.view for g in grads[0]],
+                          mean=None if rms else d["m"].view, dbias=[g.view for g in grads[1]] if has_bias else None,
+                          dh=d["dh"].view if has_dh else None, dx=dx and dx.view, kind=kind, dropout=_drop(p),
+                          accumulate=add)
+
+    call()
+    if not add:
+        first = [bits(g.view) for s in range(1 + has_bias) for g in grads[s]]
+        call()
+        assert all(np.array_equal(a, bits(g.view)) for a, g in
+                   zip(first, [g for s in range(1 + has_bias) for g in grads[s]]))
+    torch.cuda.synchronize()
+    assert dres.guards_intact() and all(g.guards_intact() for s in grads for g in s) and (not dx or dx.guards_intact())
+    want = T.norm_grad(dy, h, m, r, w, dh, rms)[0]
+    K = _depth(E)
+    xhat, g = (h - m[:, None]) * r[:, None], dy * w
+    mean = lambda v: v.mean(1, keepdims=True) if v.size else v  # noqa: E731
+    tol = r[:, None] * U * ((K + 8) * (mean(np.abs(g)) + np.abs(xhat) * mean(np.abs(g * xhat))) + 8 * np.abs(g))
+    tol = tol + 3 * U * np.abs(want) + (3 * U * np.abs(dh) if has_dh else 0)
+    _close("dres", _host(dres.view), want, (tol + HALF[act] * np.abs(want)) * 1.01 + TINY[act])
+    if p:
+        f = _factors(R * n, E, p)
+        _close("dx", _host(dx.view), want * f, ((tol + (HALF[act] + 2 * U) * np.abs(want)) * f) * 1.01 + TINY[act])
+    for k in range(R):
+        at = slice(k * n, (k + 1) * n)
+        _, dw, db, aw, ab = T.norm_grad(dy[at], h[at], m[at], r[at], w, None, rms)
+        for s, (v, a) in enumerate(((dw, aw), (db, ab))):
+            if s and not has_bias:
+                continue
+            t = (n + 8) * U * a
+            if add:
+                v, t = v + old[s, k], t + U * np.abs(v + old[s, k])
+            _close(f"grad {s} of rank {k}", _host(grads[s][k].view), v, (t + HALF[gd] * np.abs(v)) * 1.01 + TINY[gd])
+
+
+def test_norm_gradient_is_the_difference_quotient():
+    """fp32 gradients against central differences of the oracle's forward
+    pass, sum(c y) + sum(e h) along a direction, step 1e-4 (truncation and
+    rounding below 1e-6 here)."""
+    require_gpu()
+    note("[norm_grad] differences")
+    rng = _rng(6)
+    n, E, eps = 4, 53, 1e-3
+    h, c, e, v, w, b = (_values(rng, s, "f32") for s in ((n, E),) * 4 + ((E,),) * 2)
+    dh, dy, de, dw_, db_ = (_dev(a, "f32") for a in (h, c, e, w, b))
+    y, mean, rstd, dres = _out((n, E), "f32"), _out((n,), "f32"), _out((n,), "f32"), _out((n, E), "f32")
+    gw, gb = _out((E,), "f32"), _out((E,), "f32")
+    hp.fsdp_norm(dh.view, dw_.view, y.view, bias=db_.view, mean=mean.view, rstd=rstd.view, eps=eps)
+    hp.fsdp_norm_grad(dy.view, dh.view, rstd.view, dw_.view, dres.view, [gw.view], mean=mean.view, dbias=[gb.view],
+                      dh=de.view)
+    ef = float(np.float32(eps))
+
+    def loss(h, w, b):
+        return (c * T.norm(h, w, b, ef, False)[0]).sum() + (e * h).sum()
+
+    s = 1e-4
+    vw, vb = rng.standard_normal(E), rng.standard_normal(E)
+    for got, x, k in ((_host(dres.view), v, 0), (_host(gw.view), vw, 1), (_host(gb.view), vb, 2)):
+        plus, minus = [h, w, b], [h, w, b]
+        plus[k], minus[k] = plus[k] + s * x, minus[k] - s * x
+        diff = (loss(*plus) - loss(*minus)) / (2 * s)
+        # the gradient's elements are below 10 and off by at most 100 U of that
+        assert abs(diff - (got * x).sum()) <= 1e-6 + 100 * U * 10 * np.abs(x).sum()
+
+
+# --- values --------------------------------------------------------------------
+
+def test_dropped_infinities_and_nan_leave_nothing():
+    """Where the mask drops an element its value does not matter, forward and
+    backward; a NaN that is kept stays in its own row."""
+    require_gpu()
+    note("[values] dropped inf and nan")
+    rng = _rng(7)
+    n, E, p = 6, 40, 0.5
+    f = _factors(n, E, p)
+    x, w = _values(rng, (n, E), "f32"), _values(rng, (E,), "f32", 0.3, 1.0)
+    bad = x.copy()
+    bad[f == 0] = np.resize([np.inf, -np.inf, np.nan], (f == 0).sum())
+    outs = []
+    for a in (x, bad):
+        dx, dw = _dev(a, "f32"), _dev(w, "f32")
+        h, y = _out((n, E), "f32"), _out((n, E), "f32")
+        hp.fsdp_norm(dx.view, dw.view, y.view, h=h.view, dropout=_drop(p))
+        tok, table, out = torch.arange(n, device="cuda"), dx, _out((n, E), "f32")
+        hp.fsdp_embedding(tok, table.view, out.view, dropout=_drop(p))
+        g = _out((2, E), "f32")
+        hp.fsdp_embedding_grad(torch.tensor([0, 1, 1, 0, 1, 0], device="cuda"), dx.view, [g.view], dropout=_drop(p))
+        outs.append([bits(t.view) for t in (h, y, out, g)])
+    assert all(np.array_equal(a, b) for a, b in zip(*outs))
+    x[2, 3] = np.nan
+    dx, dw, y = _dev(x, "f32"), _dev(w, "f32"), _out((n, E), "f32")
+    hp.fsdp_norm(dx.view, dw.view, y.view)
+    got = np.isnan(_host(y.view)).all(1)
+    assert got.tolist() == [k == 2 for k in range(n)] and not np.isnan(_host(y.view)[[0, 1, 3, 4, 5]]).any()
+
+
+@pytest.mark.parametrize("cols", [9, 640, 4100])
+def test_constant_and_tiny_rows(cols):
+    """Rows without variance give bias (their deviation from the mean is
+    exactly zero), and rows of the smallest numbers stay finite."""
+    require_gpu()
+    note(f"[values] constant rows {cols}")
+    x = torch.full((3, cols), 3.0, device="cuda")
+    x[1] = 2.0 ** -149
+    x[2] = 0.0
+    w, b = torch.ones(cols, device="cuda"), torch.randn(cols, device="cuda")
+    y, rstd = torch.empty_like(x), torch.empty(3, device="cuda")
+    hp.fsdp_norm(x, w, y, bias=b, rstd=rstd)
+    assert torch.equal(y[0], b) and torch.equal(y[2], b) and bool(torch.isfinite(y).all())
+    _close("rstd", _host(rstd), np.full(3, float(np.float32(1e-5)) ** -0.5), 8 * U * 320)
+
+
+def test_seed_step_and_site_change_the_mask():
+    require_gpu()
+    note("[dropout] seed, step, site, rounding of p")
+    table = torch.ones(1, 4096, device="cuda")
+    tok, out = torch.zeros(4, dtype=torch.int64, device="cuda"), torch.empty(4, 4096, device="cuda")
+
+    def mask(p, seed, step, site):
+        hp.fsdp_embedding(tok, table, out, dropout=hp.Dropout(p, _state(seed, step), site))
+        return out.clone()
+
+    base = mask(0.5, 5, 1, 0)
+    assert torch.equal(base, mask(0.5, 5, 1, 0)) and torch.equal(base, mask(0.5, 5, 1 + (1 << 32), 0))
+    for other in ((0.5, 6, 1, 0), (0.5, 5 + (1 << 40), 1, 0), (0.5, 5, 2, 0), (0.5, 5, 1, 1)):
+        assert not torch.equal(base, mask(*other))
+    assert not torch.equal(base[0], base[1])  # rows differ
+    assert bool((mask(2.0 ** -18, 5, 1, 0) == 1).all())  # p rounds to 0: all kept, unscaled
+    # the largest p: kept elements are scaled by 65536
+    top = mask(65535 / 65536, 5, 1, 0)
+    assert set(top.unique().tolist()) <= {0.0, 65536.0}
+
+
+# --- addresses -------------------------------------------------------------------
+
+def test_offsets_beyond_32_bits():
+    """Tables, activations and gradients of more than 2^32 elements."""
+    require_gpu()
+    note("[offsets] embedding")
+    V, E = 70001, 65537  # 4.59e9 elements
+    table = torch.zeros(V, E, dtype=torch.bfloat16, device="cuda")
+    row = torch.randn(E, device="cuda").to(torch.bfloat16)
+    table[V - 1] = row
+    table[65536] = -row
+    out = torch.empty(3, E, dtype=torch.bfloat16, device="cuda")
+    hp.fsdp_embedding(torch.tensor([V - 1, 0, 65536], device="cuda"), table, out)
+    assert torch.equal(out[0], row) and not bool(out[1].any()) and torch.equal(out[2], -row)
+    note("[offsets] embedding_grad")
+    table.fill_(1.0)
+    tok = torch.full((200,), V - 1, device="cuda")
+    tok[:3] = torch.tensor([65536, 65535, 65536])
+    dout = torch.ones(200, E, dtype=torch.bfloat16, device="cuda")
+    hp.fsdp_embedding_grad(tok, dout, [table])
+    assert bool((table[V - 1] == 197).all()) and bool((table[65536] == 2).all()) and bool((table[65535] == 1).all())
+    assert not bool(table[:65535].any()) and not bool(table[65537:V - 1].any())
+    del table
+    note("[offsets] norm")
+    n, E = 1100001, 4096  # 4.5e9 elements
+    x = torch.zeros(n, E, dtype=torch.bfloat16, device="cuda")
+    x[-5:] = torch.randn(5, E, device="cuda").to(torch.bfloat16)
+    w, y = torch.randn(E, device="cuda"), torch.empty_like(x)
+    mean, rstd = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    hp.fsdp_norm(x, w, y, mean=mean, rstd=rstd)
+    tail = torch.empty(5, E, dtype=torch.bfloat16, device="cuda")
+    hp.fsdp_norm(x[-5:], w, tail)
+    assert torch.equal(y[-5:], tail) and not bool(y[-10:-5].any())
+    note("[offsets] norm_grad")
+    dres, gw = torch.empty_like(x), torch.empty(E, device="cuda")
+    hp.fsdp_norm_grad(y, x, rstd, w, dres, [gw], mean=mean)
+    want, gt = torch.empty_like(tail), torch.empty(E, device="cuda")
+    hp.fsdp_norm_grad(tail, x[-5:], rstd[-5:], w, want, [gt], mean=mean[-5:])
+    assert torch.equal(dres[-5:], want)
+    # the other rows add zeros: 5 terms a column, in any order
+    assert bool(((gw - gt).abs() <= 10 * U * 5 * (tail.float() * 8).abs().amax(0).clamp_min(1) * 8).all())
+
+
+# --- streams, captures, one run of them together -------------------------------------
+
+def _ops(n, V, E, seed):
+    """The four operators on one set of buffers: (inputs to refill, outputs, the calls)."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    tok = torch.randint(0, V, (2, n // 2), device="cuda", generator=gen)
+    bf = lambda *s: torch.randn(s, device="cuda", generator=gen).to(torch.bfloat16)  # noqa: E731
+    empty = lambda *s, dt=torch.bfloat16: torch.empty(s, dtype=dt, device="cuda")  # noqa: E731
+    state = _state(seed, 3)
+    table, w, b, res, dy, dh = bf(V, E), bf(E), bf(E), bf(n, E), bf(n, E), bf(n, E)
+    x, h, y, dres, dx = (empty(n, E) for _ in range(5))
+    mean, rstd = empty(n, dt=torch.float32), empty(n, dt=torch.float32)
+    gw, gb = ([empty(E, dt=torch.float32) for _ in range(2)] for _ in range(2))
+    gt = [empty(V, E, dt=torch.float32) for _ in range(2)]
+    d0, d1 = hp.Dropout(0.1, state, 0), hp.Dropout(0.2, state, 1)
+
+    def run(stream=None):
+        hp.fsdp_embedding(tok, table, x, scale=2.0, dropout=d0, stream=stream)
+        hp.fsdp_norm(x, w, y, bias=b, residual=res, h=h, mean=mean, rstd=rstd, dropout=d1, stream=stream)
+        hp.fsdp_norm_grad(dy, h, rstd, w, dres, gw, mean=mean, dbias=gb, dh=dh, dx=dx, dropout=d1, stream=stream)
+        hp.fsdp_embedding_grad(tok, dx, gt, scale=2.0, dropout=d0, stream=stream)
+
+    def refill(k):
+        gen.manual_seed(1000 * seed + k)
+        tok.random_(0, V, generator=gen)
+        for t in (table, res, dy, dh):
+            t.copy_(torch.randn(t.shape, device="cuda", generator=gen))
+        state[1] += 1
+
+    outs = [x, h, y, mean, rstd, dres, dx] + gw + gb + gt
+    return run, refill, outs
+
+
+def _eager(run, outs):
+    run()
+    torch.cuda.synchronize()
+    return [t.clone() for t in outs]
+
+
+def test_on_other_streams():
+    """The calls on a side stream, by its torch object and by its handle,
+    against the current stream's results."""
+    require_gpu()
+    note("[streams] side stream")
+    run, refill, outs = _ops(300, 700, 264, 1)
+    want = _eager(run, outs)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, 0):
+        for t in outs:
+            t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        run(stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    with torch.cuda.stream(side):
+        for t in outs:
+            t.fill_(float("nan"))
+        run()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_captured_and_replayed():
+    """A graph of first calls of their sizes (nothing was issued before the
+    capture), replayed with new inputs, another step of the dropout and the
+    program's own work between the replays, each against the eager result."""
+    require_gpu()
+    note("[capture] replays")
+    run, refill, outs = _ops(310, 650, 392, 2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for k in range(4):
+        refill(k)
+        for t in outs:
+            t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs]
+        want = _eager(run, outs)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), k
+        scratch = torch.randn(1 << 20, device="cuda")  # the program's own allocations
+        del scratch
+
+
+def test_two_graphs_replayed_at_once():
+    """Two captures of the same sizes on two streams: their workspaces are
+    their own."""
+    require_gpu()
+    note("[capture] two graphs at once")
+    made = [_ops(2000, 300, 520, s) for s in (3, 4)]
+    want = [_eager(run, outs) for run, _, outs in made]
+    graphs = []
+    for run, _, _ in made:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for rep in range(3):
+        for _, _, outs in made:
+            for t in outs:
+                t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for (_, _, outs), w in zip(made, want):
+            assert all(torch.equal(a, b) for a, b in zip(outs, w)), rep
+
+
+def test_prepared_calls():
+    require_gpu()
+    note("[prepare] calls issued again")
+    n, V, E = 130, 90, 72
+    tok = torch.randint(0, V, (n,), device="cuda")
+    dout = torch.randn(n, E, device="cuda")
+    a, b = torch.empty(V, E, device="cuda"), torch.empty(V, E, device="cuda")
+    call = hp.prepare(hp.fsdp_embedding_grad, tok, dout, [a], scale=3.0)
+    for k in range(3):
+        dout.normal_()
+        call()
+        hp.fsdp_embedding_grad(tok, dout, [b], scale=3.0)
+        assert torch.equal(a, b), k
+    y, rstd, w = torch.empty_like(dout), torch.empty(n, device="cuda"), torch.ones(E, device="cuda")
+    norm = hp.prepare("fsdp_norm", dout, w, y, rstd=rstd, kind=hp.RMS)
+    norm()
+    other = torch.empty_like(y)
+    hp.fsdp_norm(dout, w, other, kind=hp.RMS)
+    assert torch.equal(y, other)
+    g0, g1, d0, d1 = torch.empty_like(w), torch.empty_like(w), torch.empty_like(y), torch.empty_like(y)
+    hp.prepare(hp.fsdp_norm_grad, y, dout, rstd, w, d0, [g0], kind=hp.RMS)()
+    hp.fsdp_norm_grad(y, dout, rstd, w, d1, [g1], kind=hp.RMS)
+    torch.cuda.synchronize()
+    assert torch.equal(g0, g1) and torch.equal(d0, d1)
+
+
+def test_time_next_launch_covers_the_call():
+    require_gpu()
+    note("[timing] fsdp_time_next_launch")
+    run, _, outs = _ops(2000, 3000, 1024, 5)
+    run()
+    start, stop = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record(), stop.record()
+    torch.cuda.synchronize()
+    x = torch.randn(2000, 1024, device="cuda")
+    y, rstd, w = torch.empty_like(x), torch.empty(2000, device="cuda"), torch.ones(1024, device="cuda")
+    gw = torch.empty(1024, device="cuda")
+    hp.fsdp_norm(x, w, y, rstd=rstd, kind=hp.RMS)
+    hp.fsdp_time_next_launch(start, stop)
+    hp.fsdp_norm_grad(y, x, rstd, w, torch.empty_like(x), [gw], kind=hp.RMS)
+    torch.cuda.synchronize()
+    assert 0 < start.elapsed_time(stop) < 5

@@ -1,0 +1,238 @@
+"""Token operators without a GPU: the float64 oracle against published
+vectors, torch's float64 operators and differences, and the library's refusals
+(every argument is checked before anything is enqueued; the addresses here are
+fake and never dereferenced)."""
+
+import ctypes
+import json
+import os
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import token_oracle as T
+
+hp = pytest.importorskip("hsdp_parameter_gradient_amd")
+from hsdp_parameter_gradient_amd import _binding as B  # noqa: E402
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+# --- the oracle ---------------------------------------------------------------
+
+@pytest.mark.parametrize("counter,key,rounds,want", [
+    # the generator's published known answers
+    ((0, 0, 0, 0), (0, 0), 7, (0x5F6FB709, 0x0D893F64, 0x4F121F81, 0x4F730A48)),
+    ((0xFFFFFFFF,) * 4, (0xFFFFFFFF,) * 2, 7, (0x5207DDC2, 0x45165E59, 0x4D8EE751, 0x8C52F662)),
+    ((0x243F6A88, 0x85A308D3, 0x13198A2E, 0x03707344), (0xA4093822, 0x299F31D0), 7,
+     (0x4DFCCABA, 0x190A87F0, 0xC47362BA, 0xB6B5242A)),
+    ((0, 0, 0, 0), (0, 0), 10, (0x6627E8D5, 0xE169C58D, 0xBC57AC4C, 0x9B00DBD8)),
+])
+def test_philox_known_answers(counter, key, rounds, want):
+    assert T.philox4x32(counter, key, rounds) == want
+
+
+def test_dropout_keeps_its_share():
+    """10^5 elements at p = 0.25: the share kept is within 5 standard
+    deviations, sqrt(p (1 - p) / n), of 1 - p; the factor is 1 / (1 - p)."""
+    f = T.dropout_factors(100, 1000, 0.25, 1234567890123, 5, 2)
+    assert set(np.unique(f)) == {0.0, 4 / 3}
+    assert abs((f != 0).mean() - 0.75) < 5 * np.sqrt(0.25 * 0.75 / f.size)
+    assert not np.array_equal(f, T.dropout_factors(100, 1000, 0.25, 1234567890123, 6, 2))
+    assert not np.array_equal(f, T.dropout_factors(100, 1000, 0.25, 1234567890123, 5, 3))
+
+
+@pytest.mark.parametrize("name,dtype", [("f32", torch.float32), ("bf16", torch.bfloat16), ("f16", torch.float16)])
+def test_round_to_is_torch_rounding(name, dtype):
+    a = np.random.default_rng(3).standard_normal(4000) * np.exp(np.random.default_rng(4).uniform(-20, 10, 4000))
+    a = np.concatenate([a, [0.0, 1.5, -2.0 ** -24, 2.0 ** -25, 65504.0]])
+    assert np.array_equal(T.round_to(a, name), torch.from_numpy(a).to(dtype).double().numpy())
+
+
+def test_oracle_matches_torch_in_float64():
+    rng = np.random.default_rng(11)
+    h, w, b, dy = (rng.standard_normal(s) for s in ((6, 37), (37,), (37,), (6, 37)))
+    for rms in (False, True):
+        th, tw, tb = (torch.tensor(v, requires_grad=True) for v in (h, w, b))
+        ty = torch.nn.functional.rms_norm(th, (37,), tw, 1e-3) + tb if rms else \
+            torch.nn.functional.layer_norm(th, (37,), tw, tb, 1e-3)
+        ty.backward(torch.tensor(dy))
+        y, mean, rstd = T.norm(h, w, b, 1e-3, rms)
+        d, dw, db, _, _ = T.norm_grad(dy, h, mean, rstd, w, None, rms)
+        for got, want in ((y, ty.detach()), (d, th.grad), (dw, tw.grad), (db, tb.grad)):
+            np.testing.assert_allclose(got, want.numpy(), rtol=1e-11, atol=1e-12)
+    table, tok, dout = rng.standard_normal((9, 5)), np.array([3, 3, 0, 8]), rng.standard_normal((4, 5))
+    tt = torch.tensor(table, requires_grad=True)
+    e = torch.nn.functional.embedding(torch.tensor(tok), tt) * 3.0
+    e.backward(torch.tensor(dout))
+    np.testing.assert_allclose(T.embedding(tok, table, 3.0), e.detach().numpy(), rtol=1e-14)
+    np.testing.assert_allclose(T.embedding_grad(tok, dout, 9, 3.0)[0], tt.grad.numpy(), rtol=1e-14)
+    # tokens outside the table
+    assert not T.embedding([-1, 9, -2 ** 63], table).any()
+    assert not T.embedding_grad([-1, 9, 2 ** 62, 9], dout, 9)[0].any()
+
+
+@pytest.mark.parametrize("rms", [False, True])
+def test_oracle_norm_gradient_is_the_difference_quotient(rms):
+    """Central differences of sum(c * y) and of sum(e * h) along a direction:
+    step 1e-4, so a truncation of about 1e-8 and a rounding of about 1e-11."""
+    rng = np.random.default_rng(21)
+    h, w, b, c, e, v = (rng.standard_normal(s) for s in ((3, 11), (11,), (11,), (3, 11), (3, 11), (3, 11)))
+
+    def loss(x):
+        return (c * T.norm(x, w, b, 1e-3, rms)[0]).sum() + (e * x).sum()
+
+    _, mean, rstd = T.norm(h, w, b, 1e-3, rms)
+    d = T.norm_grad(c, h, mean, rstd, w, e, rms)[0]
+    s = 1e-4
+    assert abs((loss(h + s * v) - loss(h - s * v)) / (2 * s) - (d * v).sum()) < 1e-6
+
+
+# --- refusals -----------------------------------------------------------------
+
+BASE = 1 << 40  # fake, never dereferenced
+
+
+def _ptrs(vals):
+    return (ctypes.c_void_p * len(vals))(*[v or None for v in vals])
+
+
+def _drop(p=0.5, site=0, state=BASE + (9 << 32)):
+    return ctypes.byref(B._Dropout(p, site, state))
+
+
+def _args(order, defaults, **over):
+    assert not set(over) - set(defaults)
+    return [{**defaults, **over}[k] for k in order]
+
+
+EMB = dict(vocab=100, cols=64, table_dtype=1, out_dtype=1, table=BASE, n_tokens=10, token_bytes=8,
+           tokens=BASE + (1 << 32), scale=1.0, dropout=None, out=BASE + (2 << 32), stream=None)
+EGR = dict(n_ranks=2, vocab=100, cols=64, dtype=1, grad_dtype=0, n_tokens=10, token_bytes=8, tokens=BASE,
+           dout=BASE + (1 << 32), scale=1.0, dropout=None, accumulate=0,
+           grads=_ptrs([BASE + (2 << 32), BASE + (3 << 32)]), workspace=BASE + (4 << 32), workspace_bytes=1 << 20,
+           stream=None)
+NRM = dict(kind=0, rows=10, cols=64, dtype=1, weight_dtype=1, x=BASE, residual=BASE + (1 << 32), dropout=None,
+           weight=BASE + (2 << 32), bias=BASE + (3 << 32), eps=1e-5, h=BASE + (4 << 32), y=BASE + (5 << 32),
+           mean=BASE + (6 << 32), rstd=BASE + (7 << 32), stream=None)
+NGR = dict(kind=0, n_ranks=2, rows=10, cols=64, dtype=1, weight_dtype=1, grad_dtype=0, dy=BASE, dh=BASE + (1 << 32),
+           h=BASE + (2 << 32), mean=BASE + (3 << 32), rstd=BASE + (4 << 32), weight=BASE + (5 << 32), dropout=None,
+           accumulate=0, dres=BASE + (6 << 32), dx=BASE + (7 << 32),
+           dweight=_ptrs([BASE + (8 << 32), BASE + (8 << 32) + 4096]),
+           dbias=_ptrs([BASE + (8 << 32) + 8192, BASE + (8 << 32) + 12288]), workspace=BASE + (10 << 32),
+           workspace_bytes=1 << 24, stream=None)
+OPS = {"fsdp_embedding": EMB, "fsdp_embedding_grad": EGR, "fsdp_norm": NRM, "fsdp_norm_grad": NGR}
+
+REFUSED = [
+    ("fsdp_embedding", dict(vocab=-1), 1), ("fsdp_embedding", dict(cols=-1), 1),
+    ("fsdp_embedding", dict(n_tokens=1 << 31), 1), ("fsdp_embedding", dict(table_dtype=3), 2),
+    ("fsdp_embedding", dict(out_dtype=-1), 2), ("fsdp_embedding", dict(token_bytes=2), 1),
+    ("fsdp_embedding", dict(table=None), 1), ("fsdp_embedding", dict(table=BASE + 1), 3),
+    ("fsdp_embedding", dict(tokens=BASE + (1 << 32) + 4), 3), ("fsdp_embedding", dict(out=None), 1),
+    ("fsdp_embedding", dict(out=BASE + 64), 5), ("fsdp_embedding", dict(out=BASE + (1 << 32)), 5),
+    ("fsdp_embedding", dict(dropout=_drop(1.0)), 1), ("fsdp_embedding", dict(dropout=_drop(-0.1)), 1),
+    ("fsdp_embedding", dict(dropout=_drop(float("nan"))), 1), ("fsdp_embedding", dict(dropout=_drop(0.999999)), 1),
+    ("fsdp_embedding", dict(dropout=_drop(state=None)), 1), ("fsdp_embedding", dict(dropout=_drop(state=BASE + 4)), 3),
+    ("fsdp_embedding", dict(dropout=_drop(state=BASE + (2 << 32))), 5),
+    ("fsdp_embedding", dict(vocab=1, cols=(1 << 31) - 1, n_tokens=(1 << 31) - 1, out=1 << 12), 1),
+    ("fsdp_embedding_grad", dict(n_ranks=0), 1), ("fsdp_embedding_grad", dict(n_ranks=1 << 20), 1),
+    ("fsdp_embedding_grad", dict(dtype=7), 2), ("fsdp_embedding_grad", dict(grad_dtype=7), 2),
+    ("fsdp_embedding_grad", dict(grads=None), 1), ("fsdp_embedding_grad", dict(grads=_ptrs([BASE + (2 << 32), 0])), 1),
+    ("fsdp_embedding_grad", dict(grads=_ptrs([BASE + (2 << 32)] * 2)), 5),
+    ("fsdp_embedding_grad", dict(grads=_ptrs([BASE + (1 << 32), BASE + (2 << 32)])), 5),
+    ("fsdp_embedding_grad", dict(workspace=None), 1), ("fsdp_embedding_grad", dict(workspace=BASE + (4 << 32) + 8), 3),
+    ("fsdp_embedding_grad", dict(workspace_bytes=100), 1), ("fsdp_embedding_grad", dict(workspace=BASE + (2 << 32)), 5),
+    ("fsdp_embedding_grad", dict(token_bytes=1), 1), ("fsdp_embedding_grad", dict(dropout=_drop(2.0)), 1),
+    ("fsdp_norm", dict(kind=2), 1), ("fsdp_norm", dict(cols=0), 1), ("fsdp_norm", dict(rows=-1), 1),
+    ("fsdp_norm", dict(dtype=5), 2), ("fsdp_norm", dict(weight_dtype=5), 2), ("fsdp_norm", dict(eps=-1.0), 1),
+    ("fsdp_norm", dict(eps=float("nan")), 1), ("fsdp_norm", dict(eps=float("inf")), 1), ("fsdp_norm", dict(h=None), 1),
+    ("fsdp_norm", dict(h=None, residual=None, dropout=_drop()), 1), ("fsdp_norm", dict(y=None), 1),
+    ("fsdp_norm", dict(y=BASE), 5), ("fsdp_norm", dict(h=BASE + (1 << 32)), 5), ("fsdp_norm", dict(weight=None), 1),
+    ("fsdp_norm", dict(y=BASE + (4 << 32) + 128), 5), ("fsdp_norm", dict(rstd=BASE + (6 << 32)), 5),
+    ("fsdp_norm", dict(mean=BASE + (6 << 32) + 2), 3), ("fsdp_norm", dict(x=BASE + 1), 3),
+    ("fsdp_norm_grad", dict(kind=-1), 1), ("fsdp_norm_grad", dict(n_ranks=0), 1),
+    ("fsdp_norm_grad", dict(grad_dtype=9), 2), ("fsdp_norm_grad", dict(mean=None), 1),
+    ("fsdp_norm_grad", dict(dx=None, dropout=_drop()), 1), ("fsdp_norm_grad", dict(dweight=None), 1),
+    ("fsdp_norm_grad", dict(dbias=_ptrs([BASE + (8 << 32), BASE + (9 << 32)])), 5),
+    ("fsdp_norm_grad", dict(dres=BASE), 5), ("fsdp_norm_grad", dict(dres=BASE + (1 << 32)), 5),
+    ("fsdp_norm_grad", dict(dx=BASE + (6 << 32)), 5), ("fsdp_norm_grad", dict(workspace_bytes=16), 1),
+    ("fsdp_norm_grad", dict(workspace=None), 1), ("fsdp_norm_grad", dict(dweight=_ptrs([0, BASE + (8 << 32)])), 1),
+    ("fsdp_norm_grad", dict(rows=1 << 30, n_ranks=8, dropout=_drop()), 1),
+]
+
+
+@pytest.mark.parametrize("fn,over,code", REFUSED, ids=lambda v: str(v)[:40] if not isinstance(v, dict) else "-".join(v))
+def test_refusals(fn, over, code):
+    d = OPS[fn]
+    rc = getattr(hp.lib(), fn)(*_args(list(d), d, **over))
+    assert rc == code, (rc, hp.fsdp_last_error())
+    assert hp.fsdp_last_error()
+
+
+@pytest.mark.parametrize("fn,over", [
+    ("fsdp_embedding", dict(n_tokens=0, tokens=None, out=None)), ("fsdp_embedding", dict(cols=0)),
+    ("fsdp_embedding_grad", dict(vocab=0)), ("fsdp_embedding_grad", dict(n_tokens=0, accumulate=1, tokens=None, dout=None)),
+    ("fsdp_norm", dict(rows=0, x=None, y=None, h=None, residual=None, mean=None, rstd=None)),
+    ("fsdp_norm_grad", dict(rows=0, accumulate=1, dy=None, dh=None, h=None, mean=None, rstd=None, dres=None, dx=None)),
+], ids=lambda v: str(v)[:40] if not isinstance(v, dict) else "-".join(v))
+def test_empty_calls_enqueue_nothing(fn, over):
+    d = OPS[fn]
+    assert getattr(hp.lib(), fn)(*_args(list(d), d, **over)) == 0, hp.fsdp_last_error()
+
+
+def test_workspace_queries():
+    # offsets, order and two partial rows per 64 positions, 256-byte aligned blocks
+    assert hp.fsdp_embedding_grad_workspace(1, 64, 100, 8) == 512 + 256
+    assert hp.fsdp_embedding_grad_workspace(2, 65, 100, 8) == 1024 + 768 + 2 * 2 * 2 * 8 * 4
+    assert hp.fsdp_norm_grad_workspace(1, 0, 8) == 2 * 8 * 4
+    assert hp.fsdp_norm_grad_workspace(8, 1 << 20, 4096) % (8 * 2 * 4096 * 4) == 0
+    for call in (lambda: hp.fsdp_embedding_grad_workspace(0, 1, 1, 1), lambda: hp.fsdp_norm_grad_workspace(1, 1, 0),
+                 lambda: hp.fsdp_embedding_grad_workspace(1, -1, 1, 1), lambda: hp.fsdp_norm_grad_workspace(1, 1 << 31, 8),
+                 lambda: hp.fsdp_embedding_grad_workspace(65535, (1 << 31) - 1, 1, (1 << 31) - 1)):
+        with pytest.raises(hp.FSDPError) as e:
+            call()
+        assert e.value.code == 1
+
+
+def test_python_refusals():
+    x = torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="device tensor"):
+        hp.fsdp_norm(x, x[0], x.clone())
+    with pytest.raises(ValueError, match="last dim"):
+        hp.fsdp_norm(x, torch.zeros(7), x.clone())
+    with pytest.raises(ValueError, match="kind"):
+        hp.fsdp_norm(x, x[0], x.clone(), kind="batch")
+    with pytest.raises(ValueError, match="int64 or int32"):
+        hp.fsdp_embedding(x, x, x.clone())
+    with pytest.raises(ValueError, match="vocab, cols"):
+        hp.fsdp_embedding(torch.zeros(3, dtype=torch.int64), x[0], x.clone())
+    with pytest.raises(ValueError, match="3 elements for 2 ranks"):
+        hp.fsdp_embedding_grad(torch.zeros(3, dtype=torch.int64), x, [x, x])
+    with pytest.raises(ValueError, match="no rows of 8"):
+        hp.fsdp_embedding_grad(torch.zeros(4, dtype=torch.int64), x, [torch.zeros(9)])
+    with pytest.raises(ValueError, match="needs it"):
+        hp.fsdp_norm_grad(x, x, x[:, 0], x[0], x, [x[0]])
+    with pytest.raises(ValueError, match="one per rank"):
+        hp.fsdp_norm_grad(x, x, x[:, 0], x[0], x, [x[0]] * 3, mean=x[:, 0])
+    for p in (-0.1, 1.0, 0.999999, float("nan")):
+        with pytest.raises(ValueError, match="dropout p"):
+            hp.Dropout(p, torch.zeros(2, dtype=torch.int64))
+    with pytest.raises(ValueError, match="device tensor"):
+        hp.Dropout(0.1, torch.zeros(2, dtype=torch.int64))
+    with pytest.raises(ValueError, match="32 bits"):
+        hp.Dropout(0.1, torch.zeros(2, dtype=torch.int64), site=1 << 32)
+
+
+def test_token_kernels_use_no_scratch():
+    path = os.path.join(ROOT, "hsdp_parameter_gradient_amd", "lib", "kernel_resources.json")
+    if not os.path.exists(path):
+        pytest.skip("the library has not been built here")
+    res = json.load(open(path))
+    for k in ("embedding_kernel", "token_sort_kernel", "embedding_grad_kernel", "norm_kernel", "norm_wide_kernel",
+              "norm_grad_kernel", "norm_grad_wide_kernel", "norm_join_kernel"):
+        mine = {n: v for n, v in res.items() if k in n}
+        assert mine, f"{k} missing from the resource report"
+        for n, v in mine.items():
+            assert not v["scratch_bytes"] and not v["vgpr_spill"], (n, v)
+            assert v["lds_bytes"] <= 80 * 1024, (n, v)
