@@ -37,13 +37,13 @@ struct EmbedArgs {
   Drop drop;
 };
 
-// The gradient's workspace, per rank g (u32 words, then floats):
+// The gradient's workspace, per rank:
 //   off[V + 1]    off[v]..off[v + 1]: the sorted positions of token v
-//   order[T]      the rank's positions with a valid token, ascending by
-//                 token, positions of one token ascending
+//   order[T]      the rank's positions with a valid token, ascending by token
+//                 and position: {position, token}
 //   part[2 * pieces][cols]  partial sums of tokens with many positions
-constexpr uint32_t kPiece = 64;  // sorted positions per partial sum
-constexpr uint32_t kLong = 64;   // a token with more positions is summed in pieces
+constexpr uint32_t kPiece = 32;  // sorted positions per partial sum
+constexpr uint32_t kLong = 32;   // a token with more positions is summed in pieces
 static_assert(kLong >= kPiece, "at most two long tokens may meet a piece, the second one its end");
 
 struct EmbedGradArgs {
@@ -51,7 +51,7 @@ struct EmbedGradArgs {
   const void* dout;    // [n_ranks * n_tokens, cols]
   void* const* grads;  // host array of n_ranks device pointers
   uint32_t* off;
-  uint32_t* order;
+  uint32_t* order;  // pairs
   float* part;
   uint64_t n_tokens, vocab, cols;
   float factor;
@@ -100,7 +100,7 @@ int norm_grad_blocks(uint64_t rows, uint64_t cols, int n_ranks);
 // Whether the launches of a call stay within the largest grid.
 bool grid_fits(uint64_t blocks, uint32_t block);
 bool embedding_fits(uint64_t n_tokens, uint64_t cols);
-bool embedding_grad_fits(uint64_t n_tokens, uint64_t vocab, uint64_t cols);
+bool embedding_grad_fits(uint64_t n_tokens, uint64_t vocab, uint64_t cols, int n_ranks);
 
 }  // namespace fsdp
 

@@ -290,37 +290,53 @@ __global__ __launch_bounds__(kEmbedBlock) void embedding_kernel(fsdp::EmbedArgs 
 
 // --- embedding gradient: the positions sorted by token ------------------------
 
-// One workgroup per kSortRows tokens and rank.  It reads all of the rank's
+// One workgroup per 2^shift tokens and rank.  It reads all of the rank's
 // tokens twice (from L2), counts those of its own tokens and those below
 // them, and so knows where its part of the order begins without waiting for
 // another workgroup.  Each of its waves has a contiguous part of the
 // positions and counts apart, so that positions of one token stay ascending:
-// the order, and with it every sum, is the same on every run.
+// the order, and with it every sum, is the same on every run.  Lanes of equal
+// token find each other by one ballot per bit of the token, whatever the mix.
 constexpr int kSortBlock = 1024;
 constexpr int kSortWaves = kSortBlock / 64;
-constexpr uint32_t kSortRows = 512;
+constexpr uint32_t kSortMaxShift = 9;
+constexpr int kSortUnroll = 8;
+
+// A sorted position and its token.
+typedef u32x2 Place;
 
 __global__ __launch_bounds__(kSortBlock) void token_sort_kernel(const void* tokens, int token_bytes, uint64_t n_tokens,
-                                                                uint64_t vocab, uint32_t* off, uint32_t* order) {
-  __shared__ uint32_t cnt[kSortWaves][kSortRows];
-  __shared__ uint32_t lower, wave_sum[kSortRows / 64];
+                                                                uint64_t vocab, uint32_t shift, uint32_t* off,
+                                                                Place* order) {
+  __shared__ uint32_t cnt[kSortWaves << kSortMaxShift];
+  __shared__ uint32_t lower, wave_sum[kSortWaves];
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const uint64_t g = blockIdx.y;
-  const uint64_t v0 = (uint64_t)blockIdx.x * kSortRows;
-  const uint32_t rows = vocab - v0 < kSortRows ? (uint32_t)(vocab - v0) : kSortRows;
-  for (uint32_t i = tid; i < kSortWaves * kSortRows; i += kSortBlock) (&cnt[0][0])[i] = 0;
+  const uint64_t v0 = (uint64_t)blockIdx.x << shift;
+  const uint32_t span = 1u << shift;
+  const uint32_t rows = vocab - v0 < span ? (uint32_t)(vocab - v0) : span;
+  for (uint32_t i = tid; i < kSortWaves * span; i += kSortBlock) cnt[i] = 0;
   if (tid == 0) lower = 0;
   __syncthreads();
-  // this wave's positions
+  uint32_t* mine = cnt + (wave << shift);
+  // this wave's positions, the last wave's clipped to n_tokens
   const uint64_t per = ((n_tokens + kSortBlock - 1) / kSortBlock) * 64;
   const uint64_t begin = wave * per, end = begin + per < n_tokens ? begin + per : n_tokens;
   const uint64_t tok0 = g * n_tokens;
   uint32_t low = 0;
-  for (uint64_t t = begin + lane; t < end; t += 64) {
-    const int64_t tok = token_at(tokens, tok0 + t, token_bytes);
-    const uint64_t r = (uint64_t)tok - v0;  // wraps for a token below v0
-    low += tok >= 0 && (uint64_t)tok < v0;
-    if (tok >= 0 && (uint64_t)tok >= v0 && r < rows) atomicAdd(&cnt[wave][r], 1u);
+  for (uint64_t t0 = begin; t0 < end; t0 += 64 * kSortUnroll) {
+    int64_t tok[kSortUnroll];
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u) {
+      const uint64_t t = t0 + u * 64 + lane;
+      tok[u] = t < end ? token_at(tokens, tok0 + t, token_bytes) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u) {
+      const uint64_t r = (uint64_t)tok[u] - v0;  // wraps for a token below v0
+      low += tok[u] >= 0 && (uint64_t)tok[u] < v0;
+      if (tok[u] >= 0 && r < rows) atomicAdd(&mine[r], 1u);
+    }
   }
 #pragma unroll
   for (int s = 32; s; s >>= 1) low += __shfl_xor(low, s);
@@ -328,49 +344,55 @@ __global__ __launch_bounds__(kSortBlock) void token_sort_kernel(const void* toke
   __syncthreads();
   // exclusive prefix over the tokens, then over the waves of each token
   uint32_t total = 0, incl = 0;
-  if (tid < kSortRows) {
+  if (tid < span)
+    for (int w = 0; w < kSortWaves; ++w) total += cnt[(w << shift) + tid];
+  incl = total;
 #pragma unroll
-    for (int w = 0; w < kSortWaves; ++w) total += cnt[w][tid];
-    incl = total;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const uint32_t up = __shfl_up(incl, s);
-      if (lane >= (uint32_t)s) incl += up;
-    }
-    if (lane == 63) wave_sum[wave] = incl;
+  for (int s = 1; s < 64; s <<= 1) {
+    const uint32_t up = __shfl_up(incl, s);
+    if (lane >= (uint32_t)s) incl += up;
   }
+  if (lane == 63) wave_sum[wave] = incl;
   __syncthreads();
-  if (tid < kSortRows) {
+  if (tid < span) {
     uint32_t at = lower + incl - total;
     for (uint32_t w = 0; w < wave; ++w) at += wave_sum[w];
     uint32_t* o = off + g * (vocab + 1) + v0;
     if (tid < rows) o[tid] = at;
     if (v0 + rows == vocab && tid == rows - 1) o[rows] = at + total;
-#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      const uint32_t c = cnt[w][tid];
-      cnt[w][tid] = at;
+      const uint32_t c = cnt[(w << shift) + tid];
+      cnt[(w << shift) + tid] = at;
       at += c;
     }
   }
   __syncthreads();
-  for (uint64_t t0 = begin; t0 < end; t0 += 64) {
-    const uint64_t t = t0 + lane;
-    int64_t tok = -1;
-    if (t < end) tok = token_at(tokens, tok0 + t, token_bytes);
-    const uint64_t r64 = (uint64_t)tok - v0;
-    const bool mine = tok >= 0 && (uint64_t)tok >= v0 && r64 < rows;
-    const uint32_t r = mine ? (uint32_t)r64 : ~0u;
-    uint64_t todo = __ballot(mine);
-    while (todo) {
-      const int lead = __ffsll((unsigned long long)todo) - 1;
-      const uint32_t row = __shfl(r, lead);
-      const uint64_t same = __ballot(r == row);
+  for (uint64_t t0 = begin; t0 < end; t0 += 64 * kSortUnroll) {
+    int64_t tok[kSortUnroll];
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u) {
+      const uint64_t t = t0 + u * 64 + lane;
+      tok[u] = t < end ? token_at(tokens, tok0 + t, token_bytes) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u) {
+      const uint64_t r64 = (uint64_t)tok[u] - v0;
+      const bool in = tok[u] >= 0 && r64 < rows;
+      uint64_t same = __ballot(in);
+      if (!same) continue;
+      const uint32_t r = (uint32_t)r64;
+      for (uint32_t b = 0; b < shift; ++b) {
+        const bool bit = r >> b & 1;
+        const uint64_t m = __ballot(bit);
+        same &= bit ? m : ~m;
+      }
+      // this lane's place among its token's lanes; the first of them counts
+      const uint32_t before = __popcll(same & ((uint64_t(1) << lane) - 1));
       uint32_t at = 0;
-      if (lane == (uint32_t)lead) at = atomicAdd(&cnt[wave][row], (uint32_t)__popcll(same));
-      at = __shfl(at, lead);
-      if (r == row) order[g * n_tokens + at + __popcll(same & ((uint64_t(1) << lane) - 1))] = (uint32_t)t;
-      todo &= ~same;
+      if (in && before == 0) at = atomicAdd(&mine[r], (uint32_t)__popcll(same));
+      at = __shfl(at, in ? __ffsll((unsigned long long)same) - 1 : 0);
+      if (in)
+        gmem<Place>(order)[g * n_tokens + at + before] = Place{(uint32_t)(t0 + u * 64 + lane), (uint32_t)tok[u]};
     }
   }
 }
@@ -378,13 +400,12 @@ __global__ __launch_bounds__(kSortBlock) void token_sort_kernel(const void* toke
 // What the summing kernels see of one rank.
 struct RankView {
   const GMEM uint32_t* off;
-  const GMEM uint32_t* order;
+  const GMEM Place* order;
   uint64_t row0;  // the rank's first row of dout
 };
 
 __device__ __forceinline__ RankView rank_view(const fsdp::EmbedGradArgs& a, uint64_t g) {
-  return RankView{gmem<uint32_t>(a.off) + g * (a.vocab + 1), gmem<uint32_t>(a.order) + g * a.n_tokens,
-                  g * a.n_tokens};
+  return RankView{gmem<uint32_t>(a.off) + g * (a.vocab + 1), gmem<Place>(a.order) + g * a.n_tokens, g * a.n_tokens};
 }
 
 constexpr int kCols = 4;  // columns of a lane in the summing kernels: 16-byte fp32 stores
@@ -393,29 +414,23 @@ constexpr int kCols = 4;  // columns of a lane in the summing kernels: 16-byte f
 template <int D, bool DROP>
 __device__ __forceinline__ void sum_positions(const fsdp::EmbedGradArgs& a, const RankView& rv, const Rng& rng,
                                               uint32_t b, uint32_t e, uint64_t c, uint32_t len, float (&acc)[kCols]) {
-  uint32_t k = b;
-  for (; k + 4 <= e; k += 4) {
-    float v[4][kCols];
-    uint64_t row[4];
+  constexpr uint32_t kAhead = 8;  // rows in flight
+  for (uint32_t k = b; k < e; k += kAhead) {
+    float v[kAhead][kCols];
+    uint64_t row[kAhead];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      row[u] = rv.row0 + rv.order[k + u];
-      load_cols<D, kCols>(a.dout, row[u] * a.cols + c, len, v[u]);
-    }
+    for (uint32_t u = 0; u < kAhead; ++u)
+      if (k + u < e) {
+        row[u] = rv.row0 + rv.order[k + u][0];
+        load_cols<D, kCols>(a.dout, row[u] * a.cols + c, len, v[u]);
+      }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if constexpr (DROP) drop_cols<kCols>(rng, (uint32_t)row[u], (uint32_t)(c / kGroup), c & 4, v[u]);
+    for (uint32_t u = 0; u < kAhead; ++u)
+      if (k + u < e) {
+        if constexpr (DROP) drop_cols<kCols>(rng, (uint32_t)row[u], (uint32_t)(c / kGroup), c & 4, v[u]);
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) acc[i] += v[u][i];
-    }
-  }
-  for (; k < e; ++k) {
-    float v[kCols];
-    const uint64_t row = rv.row0 + rv.order[k];
-    load_cols<D, kCols>(a.dout, row * a.cols + c, len, v);
-    if constexpr (DROP) drop_cols<kCols>(rng, (uint32_t)row, (uint32_t)(c / kGroup), c & 4, v);
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) acc[i] += v[i];
+        for (int i = 0; i < kCols; ++i) acc[i] += v[u][i];
+      }
   }
 }
 
@@ -434,66 +449,87 @@ __device__ __forceinline__ void put_grad(const fsdp::EmbedGradArgs& a, void* gra
   store_any<kCols>(a.grad_dtype, grad, v * a.cols + c, len, out);
 }
 
-// The first `row_blocks` workgroups of a rank take (row, 4 columns) items: a
-// row of the gradient whose token has at most kLong positions is summed and
-// written at once, rows without a position included (they are written as
-// zeros).  When the gradient is added to, rows without a position stay as
-// they are, and the items are the sorted positions instead: the one that is
-// its token's first does the row.  The other workgroups sum the tokens with
-// more than kLong positions in pieces of kPiece sorted positions into `part`
-// (slot 0: the piece's first token, slot 1: its last, where that is another).
+// Three kinds of workgroups of one launch, the ones with the longest chains of
+// loads first:
+//   pieces  tokens with more than kLong positions, kPiece sorted positions at
+//           a time, into `part` (slot 0: the piece's first token, slot 1: its
+//           last, where that is another)
+//   rows    (sorted position, 4 columns) items: a position that is its
+//           token's first sums the token's whole row, unless it is a long one
+//   fill    the rows without a position, written as zeros (not when the
+//           gradient is added to): 16 bytes a lane and step
 constexpr int kGradBlock = 256;
-constexpr int kGradUnroll = 4;
+constexpr int kFillUnroll = 8;
+
+struct GradGrid {
+  uint32_t pieces, piece_cols;  // workgroups, of them per piece
+  uint32_t rows, groups, recip;
+  uint32_t fill_groups, fill_recip;
+};
 
 template <int D, bool DROP>
 __global__ __launch_bounds__(kGradBlock) void embedding_grad_kernel(fsdp::EmbedGradArgs a, fsdp::RankPtrs grads,
-                                                                    uint32_t rank0, uint32_t row_blocks,
-                                                                    uint32_t col_blocks, uint32_t groups,
-                                                                    uint32_t recip) {
+                                                                    uint32_t rank0, GradGrid grid) {
   const uint64_t g = rank0 + blockIdx.y;
   const RankView rv = rank_view(a, g);
-  Rng rng;
-  if constexpr (DROP) rng = rng_of(a.drop);
-  if (blockIdx.x < row_blocks) {
-    constexpr uint32_t kItems = kGradBlock * kGradUnroll;
-    const uint64_t first = (uint64_t)blockIdx.x * kItems;
-    const uint64_t n = (a.accumulate ? rv.off[a.vocab] : a.vocab) * groups;
-    if (first >= n) return;
-    const Split sp = split_of(first, groups, recip);
+  if (blockIdx.x >= grid.pieces + grid.rows) {
+    constexpr uint32_t kItems = kGradBlock * kFillUnroll;
+    const uint64_t first = (uint64_t)(blockIdx.x - grid.pieces - grid.rows) * kItems;
+    const uint64_t n = a.vocab * grid.fill_groups;
+    const Split sp = split_of(first, grid.fill_groups, grid.fill_recip);
+    const uint32_t es = a.grad_dtype == FSDP_F32 ? 4 : 2;
+    const uint64_t row_bytes = a.cols * es;
+    uint64_t v[kFillUnroll];
+    uint32_t j[kFillUnroll], used[kFillUnroll];
 #pragma unroll
-    for (int u = 0; u < kGradUnroll; ++u) {
+    for (int u = 0; u < kFillUnroll; ++u) {
       const uint32_t i = u * kGradBlock + threadIdx.x;
-      if (first + i >= n) break;
-      uint64_t v;
-      uint32_t j;
-      sp.at(i, v, j);
-      uint64_t at = v;
-      if (a.accumulate) {
-        v = (uint64_t)token_at(a.tokens, rv.row0 + rv.order[at], a.token_bytes);
-        if (rv.off[v] != at) continue;
+      sp.at(i, v[u], j[u]);
+      used[u] = 1;
+      if (first + i < n) used[u] = rv.off[v[u] + 1] - rv.off[v[u]];
+    }
+#pragma unroll
+    for (int u = 0; u < kFillUnroll; ++u) {
+      if (used[u]) continue;
+      const uint64_t at = v[u] * row_bytes + (uint64_t)j[u] * 16, left = row_bytes - (uint64_t)j[u] * 16;
+      if (left >= 16) {
+        *reinterpret_cast<GMEM u32x4e*>(gmem<char>(grads.p[blockIdx.y]) + at) = u32x4{0, 0, 0, 0};
+      } else {
+        for (uint64_t b = 0; b < left; b += 2) *reinterpret_cast<GMEM uint16_t*>(gmem<char>(grads.p[blockIdx.y]) + at + b) = 0;
       }
-      const uint32_t b = rv.off[v], e = rv.off[v + 1];
-      if (e - b > fsdp::kLong) continue;
-      const uint64_t c = (uint64_t)j * kCols;
-      const uint32_t len = a.cols - c < kCols ? (uint32_t)(a.cols - c) : kCols;
-      float acc[kCols] = {};
-      sum_positions<D, DROP>(a, rv, rng, b, e, c, len, acc);
-      put_grad(a, grads.p[blockIdx.y], v, c, len, acc);
     }
     return;
   }
-  const uint32_t k = blockIdx.x - row_blocks;
-  const uint32_t piece = k / col_blocks;
-  const uint64_t c = ((uint64_t)(k - piece * col_blocks) * kGradBlock + threadIdx.x) * kCols;
+  Rng rng;
+  if constexpr (DROP) rng = rng_of(a.drop);
   const uint32_t valid = rv.off[a.vocab];
+  if (blockIdx.x >= grid.pieces) {
+    const uint64_t first = (uint64_t)(blockIdx.x - grid.pieces) * kGradBlock;
+    const Split sp = split_of(first, grid.groups, grid.recip);
+    uint64_t at;
+    uint32_t j;
+    sp.at(threadIdx.x, at, j);
+    if (at >= valid) return;
+    const uint32_t v = rv.order[at][1];
+    if (at && rv.order[at - 1][1] == v) return;
+    const uint32_t e = rv.off[(uint64_t)v + 1];
+    if (e - (uint32_t)at > fsdp::kLong) return;
+    const uint64_t c = (uint64_t)j * kCols;
+    const uint32_t len = a.cols - c < kCols ? (uint32_t)(a.cols - c) : kCols;
+    float acc[kCols] = {};
+    sum_positions<D, DROP>(a, rv, rng, (uint32_t)at, e, c, len, acc);
+    put_grad(a, grads.p[blockIdx.y], v, c, len, acc);
+    return;
+  }
+  const uint32_t piece = blockIdx.x / grid.piece_cols;
+  const uint64_t c = ((uint64_t)(blockIdx.x - piece * grid.piece_cols) * kGradBlock + threadIdx.x) * kCols;
   const uint32_t k0 = piece * fsdp::kPiece;
   if (k0 >= valid || c >= a.cols) return;
   const uint32_t k1 = valid - k0 < fsdp::kPiece ? valid : k0 + fsdp::kPiece;
   const uint32_t len = a.cols - c < kCols ? (uint32_t)(a.cols - c) : kCols;
   const uint64_t pieces = (a.n_tokens + fsdp::kPiece - 1) / fsdp::kPiece;
   float* part = a.part + (g * pieces + piece) * 2 * a.cols;
-  const uint64_t va = (uint64_t)token_at(a.tokens, rv.row0 + rv.order[k0], a.token_bytes);
-  const uint64_t vb = (uint64_t)token_at(a.tokens, rv.row0 + rv.order[k1 - 1], a.token_bytes);
+  const uint64_t va = rv.order[k0][1], vb = rv.order[k1 - 1][1];
   const uint32_t ea = rv.off[va + 1];
   if (ea - rv.off[va] > fsdp::kLong) {
     float acc[kCols] = {};
@@ -524,7 +560,7 @@ __global__ __launch_bounds__(256) void embedding_join_kernel(fsdp::EmbedGradArgs
   const uint32_t k0 = piece * fsdp::kPiece;
   if (k0 >= valid) return;
   const uint32_t k1 = valid - k0 < fsdp::kPiece ? valid : k0 + fsdp::kPiece;
-  const uint64_t v = (uint64_t)token_at(a.tokens, rv.row0 + rv.order[k1 - 1], a.token_bytes);
+  const uint64_t v = rv.order[k1 - 1][1];
   const uint32_t b = rv.off[v], e = rv.off[v + 1];
   if (e - b <= fsdp::kLong || b < k0) return;  // the same for the whole workgroup
   const uint32_t last = (e - 1) / fsdp::kPiece;
@@ -533,6 +569,7 @@ __global__ __launch_bounds__(256) void embedding_join_kernel(fsdp::EmbedGradArgs
   const uint32_t len = c >= a.cols ? 0 : a.cols - c < kCols ? (uint32_t)(a.cols - c) : kCols;
   float acc[kCols] = {};
   if (len) {
+#pragma unroll 8
     for (uint32_t q = piece + wave; q <= last; q += 4) {
       float p[kCols];
       const uint64_t slot = 2 * (uint64_t)q + (q == piece && b > k0);
@@ -1065,28 +1102,54 @@ int norm_grad_go(const Launch& go, const fsdp::NormGradArgs& a) {
   return go(norm_grad_wide_kernel<D, false>, grid, 1024, true, false, a, groups);
 }
 
+// Tokens per workgroup of the sort: as few as keep all workgroups of the call
+// resident at once (two of 1024 lanes per CU), at least 16.
+uint32_t sort_shift(uint64_t vocab, int n_ranks) {
+  uint32_t s = 4;
+  while (s < kSortMaxShift && (vocab * (uint64_t)n_ranks) >> s > 512) ++s;
+  return s;
+}
+
+// The workgroups of a gradient call, per rank.
+struct GradPlan {
+  uint32_t shift;
+  uint64_t sort, pieces, piece_cols, rows, fill, join_cols;
+};
+
+GradPlan grad_plan(uint64_t n_tokens, uint64_t vocab, uint64_t cols, int n_ranks, uint64_t grad_bytes, bool accumulate) {
+  GradPlan p;
+  p.shift = sort_shift(vocab, n_ranks);
+  p.sort = ceil_div(vocab, uint64_t(1) << p.shift);
+  p.piece_cols = ceil_div(cols, kGradBlock * kCols);
+  p.join_cols = ceil_div(cols, 64 * kCols);
+  p.pieces = n_tokens > fsdp::kLong ? ceil_div(n_tokens, fsdp::kPiece) : 0;  // else no token has as many
+  p.rows = ceil_div(n_tokens * ceil_div(cols, kCols), kGradBlock);
+  p.fill = accumulate ? 0 : ceil_div(vocab * ceil_div(cols * grad_bytes, 16), kGradBlock * kFillUnroll);
+  return p;
+}
+
 template <int D, bool DROP>
 int embedding_grad_go(const Launch& go, const fsdp::EmbedGradArgs& a) {
-  int rc = go(token_sort_kernel, dim3((uint32_t)ceil_div(a.vocab, kSortRows), (uint32_t)a.n_ranks), kSortBlock, true,
-              false, a.tokens, a.token_bytes, a.n_tokens, a.vocab, a.off, a.order);
+  const uint64_t es = a.grad_dtype == FSDP_F32 ? 4 : 2;
+  const GradPlan p = grad_plan(a.n_tokens, a.vocab, a.cols, a.n_ranks, es, a.accumulate);
+  int rc = go(token_sort_kernel, dim3((uint32_t)p.sort, (uint32_t)a.n_ranks), kSortBlock, true, false, a.tokens,
+              a.token_bytes, a.n_tokens, a.vocab, p.shift, a.off, reinterpret_cast<Place*>(a.order));
   if (rc) return rc;
-  const uint64_t groups = ceil_div(a.cols, kCols);
-  const uint64_t row_blocks = ceil_div((a.accumulate ? a.n_tokens : a.vocab) * groups, kGradBlock * kGradUnroll);
-  const bool pieces = a.n_tokens > fsdp::kLong;  // else no token has more positions
-  const uint64_t n_pieces = pieces ? ceil_div(a.n_tokens, fsdp::kPiece) : 0;
-  const uint64_t cb = ceil_div(a.cols, kGradBlock * kCols), cj = ceil_div(a.cols, 64 * kCols);
+  const uint64_t groups = ceil_div(a.cols, kCols), fill_groups = ceil_div(a.cols * es, 16);
+  const GradGrid grid{(uint32_t)(p.pieces * p.piece_cols), (uint32_t)p.piece_cols, (uint32_t)p.rows, (uint32_t)groups,
+                      recip_of(groups), (uint32_t)fill_groups, recip_of(fill_groups)};
+  const uint32_t blocks = (uint32_t)(p.pieces * p.piece_cols + p.rows + p.fill);
   for (int g0 = 0; g0 < a.n_ranks; g0 += fsdp::kMaxRankPtrs) {
     const int n = a.n_ranks - g0 < fsdp::kMaxRankPtrs ? a.n_ranks - g0 : fsdp::kMaxRankPtrs;
     const bool end = g0 + n == a.n_ranks;
     fsdp::RankPtrs ptrs = {};
     for (int k = 0; k < n; ++k) ptrs.p[k] = a.grads[g0 + k];
-    rc = go(embedding_grad_kernel<D, DROP>, dim3((uint32_t)(row_blocks + n_pieces * cb), (uint32_t)n), kGradBlock,
-            false, end && !pieces, a, ptrs, (uint32_t)g0, (uint32_t)row_blocks, (uint32_t)cb, (uint32_t)groups,
-            recip_of(groups));
+    rc = go(embedding_grad_kernel<D, DROP>, dim3(blocks, (uint32_t)n), kGradBlock, false, end && !p.pieces, a, ptrs,
+            (uint32_t)g0, grid);
     if (rc) return rc;
-    if (pieces) {
-      rc = go(embedding_join_kernel, dim3((uint32_t)(n_pieces * cj), (uint32_t)n), 256, false, end, a, ptrs,
-              (uint32_t)g0, (uint32_t)cj);
+    if (p.pieces) {
+      rc = go(embedding_join_kernel, dim3((uint32_t)(p.pieces * p.join_cols), (uint32_t)n), 256, false, end, a, ptrs,
+              (uint32_t)g0, (uint32_t)p.join_cols);
       if (rc) return rc;
     }
   }
@@ -1115,12 +1178,10 @@ bool fsdp::embedding_fits(uint64_t n_tokens, uint64_t cols) {
   return grid_fits(ceil_div(n_tokens * ceil_div(cols, kGroup), kEmbedBlock * kEmbedUnroll), kEmbedBlock);
 }
 
-bool fsdp::embedding_grad_fits(uint64_t n_tokens, uint64_t vocab, uint64_t cols) {
-  const uint64_t rows = vocab > n_tokens ? vocab : n_tokens, pieces = ceil_div(n_tokens, kPiece);
-  return grid_fits(ceil_div(vocab, kSortRows), kSortBlock) &&
-         grid_fits(ceil_div(rows * ceil_div(cols, kCols), kGradBlock * kGradUnroll) +
-                       pieces * ceil_div(cols, kGradBlock * kCols), kGradBlock) &&
-         grid_fits(pieces * ceil_div(cols, 64 * kCols), 256);
+bool fsdp::embedding_grad_fits(uint64_t n_tokens, uint64_t vocab, uint64_t cols, int n_ranks) {
+  const GradPlan p = grad_plan(n_tokens, vocab, cols, n_ranks, 4, false);
+  return grid_fits(p.sort, kSortBlock) && grid_fits(p.pieces * p.piece_cols + p.rows + p.fill, kGradBlock) &&
+         grid_fits(p.pieces * p.join_cols, 256);
 }
 
 int fsdp_launch_embedding(const fsdp::EmbedArgs& a, void* stream, void* start_event, void* stop_event) {

@@ -141,7 +141,7 @@ int grad_workspace(int32_t n_ranks, int64_t n_tokens, int64_t vocab, int64_t col
   const int64_t pieces = n_tokens > fsdp::kLong ? (n_tokens + fsdp::kPiece - 1) / fsdp::kPiece : 0;
   int64_t part;
   w->order_at = up(4 * (vocab + 1) * n_ranks);
-  w->part_at = w->order_at + up(4 * n_tokens * n_ranks);
+  w->part_at = w->order_at + up(8 * n_tokens * n_ranks);
   if (!mul_ok(pieces * 8, cols, &part) || !mul_ok(part, n_ranks, &part) || !add_ok(w->part_at, part, &w->bytes))
     return fail(FSDP_EINVAL, "workspace size overflow");
   return FSDP_OK;
@@ -184,7 +184,7 @@ int embedding_grad_impl(int32_t n_ranks, int64_t vocab, int64_t cols, int32_t dt
   double keep;
   if ((rc = make_drop(dropout, rows, &b, &a.drop, &keep)) || (rc = b.check())) return rc;
   if (vocab == 0 || cols == 0 || (accumulate && n_tokens == 0)) return ok();
-  if (!fsdp::embedding_grad_fits(n_tokens, vocab, cols))
+  if (!fsdp::embedding_grad_fits(n_tokens, vocab, cols, n_ranks))
     return fail(FSDP_EINVAL, "vocab * cols or n_tokens * cols too large for one call");
   a.tokens = tokens;
   a.dout = dout;
