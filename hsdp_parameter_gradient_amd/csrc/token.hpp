@@ -40,20 +40,21 @@ struct EmbedArgs {
 // The gradient's workspace, per rank:
 //   off[V + 1]    off[v]..off[v + 1]: the sorted positions of token v
 //   order[T]      the rank's positions with a valid token, ascending by token
-//                 and position: {position, token}
+//                 and position, four words each (Place)
 //   part[2 * pieces][cols]  partial sums of tokens with many positions
-constexpr uint32_t kPiece = 32;  // sorted positions per partial sum
-constexpr uint32_t kLong = 32;   // a token with more positions is summed in pieces
-static_assert(kLong >= kPiece, "at most two long tokens may meet a piece, the second one its end");
+constexpr uint32_t kMaxPiece = 32, kMinPiece = 4;  // sorted positions per partial sum
+constexpr uint32_t kLong = 32;  // a token with more positions is summed in pieces
+static_assert(kLong >= kMaxPiece, "at most two long tokens may meet a piece, the second one its end");
 
 struct EmbedGradArgs {
   const void* tokens;  // [n_ranks, n_tokens]
   const void* dout;    // [n_ranks * n_tokens, cols]
   void* const* grads;  // host array of n_ranks device pointers
   uint32_t* off;
-  uint32_t* order;  // pairs
+  uint32_t* order;  // four words each
   float* part;
   uint64_t n_tokens, vocab, cols;
+  uint32_t piece;  // embedding_grad_piece
   float factor;
   int n_ranks, dtype, grad_dtype, token_bytes, accumulate;
   Drop drop;
@@ -96,6 +97,10 @@ struct NormGradArgs {
 // partial sums per rank): a function of the sizes only, so that the order of
 // every sum is fixed.
 int norm_grad_blocks(uint64_t rows, uint64_t cols, int n_ranks);
+
+// Sorted positions per piece: as many as still give every SIMD of the chip
+// several waves.
+uint32_t embedding_grad_piece(uint64_t n_tokens, uint64_t cols, int n_ranks);
 
 // Whether the launches of a call stay within the largest grid.
 bool grid_fits(uint64_t blocks, uint32_t block);

@@ -247,6 +247,16 @@ uint32_t recip_of(uint64_t groups) {
   return groups > 1 && groups <= kMaxRecipGroups ? (uint32_t)((uint64_t(1) << 32) / groups + 1) : 0;
 }
 
+// Workgroups are dealt to the 8 XCDs in turn.  Within every group of 8 * RUN
+// of them, XCD x takes RUN consecutive ones, so that each XCD writes runs of
+// contiguous memory; a bijection on [0, n), the last partial group in plain
+// order.
+template <uint32_t RUN>
+__device__ __forceinline__ uint32_t xcd_order(uint32_t b, uint32_t n) {
+  const uint32_t base = b / (8 * RUN) * (8 * RUN), r = b - base;
+  return n - base < 8 * RUN ? b : base + (r % 8) * RUN + r / 8;
+}
+
 // --- embedding ------------------------------------------------------------------
 
 // out[t] = drop(factor * table[token[t]]): one pass, bound by reading the
@@ -291,24 +301,31 @@ __global__ __launch_bounds__(kEmbedBlock) void embedding_kernel(fsdp::EmbedArgs 
 // --- embedding gradient: the positions sorted by token ------------------------
 
 // One workgroup per 2^shift tokens and rank.  It reads all of the rank's
-// tokens twice (from L2), counts those of its own tokens and those below
-// them, and so knows where its part of the order begins without waiting for
-// another workgroup.  Each of its waves has a contiguous part of the
-// positions and counts apart, so that positions of one token stay ascending:
-// the order, and with it every sum, is the same on every run.  Lanes of equal
-// token find each other by one ballot per bit of the token, whatever the mix.
+// tokens (from L2), counts those of its own tokens and those below them, and
+// so knows where its part of the order begins without waiting for another
+// workgroup.  Each of its waves has a contiguous part of the positions,
+// counts apart and lists its matches in order, so that positions of one token
+// stay ascending: the order, and with it every sum, is the same on every run.
+// Then it places its lists: lanes of equal token find each other by one
+// ballot per bit of the token, whatever the mix.  A wave with more matches
+// than its list holds reads its tokens again.
 constexpr int kSortBlock = 1024;
 constexpr int kSortWaves = kSortBlock / 64;
 constexpr uint32_t kSortMaxShift = 9;
 constexpr int kSortUnroll = 8;
+constexpr uint32_t kSortList = 512;  // matches listed per wave
+constexpr uint32_t kSortMaxPart = 1u << (32 - kSortMaxShift);  // a listed match is (position in the wave's part, row)
 
-// A sorted position and its token.
-typedef u32x2 Place;
+// A sorted position: {position, token, how many positions the token has, the
+// index of the first of them}.
+typedef u32x4 Place;
 
 __global__ __launch_bounds__(kSortBlock) void token_sort_kernel(const void* tokens, int token_bytes, uint64_t n_tokens,
                                                                 uint64_t vocab, uint32_t shift, uint32_t* off,
                                                                 Place* order) {
   __shared__ uint32_t cnt[kSortWaves << kSortMaxShift];
+  __shared__ uint32_t first[1 << kSortMaxShift], count[1 << kSortMaxShift];
+  __shared__ uint32_t list[kSortWaves][kSortList];
   __shared__ uint32_t lower, wave_sum[kSortWaves];
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const uint64_t g = blockIdx.y;
@@ -319,11 +336,12 @@ __global__ __launch_bounds__(kSortBlock) void token_sort_kernel(const void* toke
   if (tid == 0) lower = 0;
   __syncthreads();
   uint32_t* mine = cnt + (wave << shift);
+  const uint64_t below = (uint64_t(1) << lane) - 1;
   // this wave's positions, the last wave's clipped to n_tokens
   const uint64_t per = ((n_tokens + kSortBlock - 1) / kSortBlock) * 64;
   const uint64_t begin = wave * per, end = begin + per < n_tokens ? begin + per : n_tokens;
   const uint64_t tok0 = g * n_tokens;
-  uint32_t low = 0;
+  uint32_t low = 0, listed = 0;
   for (uint64_t t0 = begin; t0 < end; t0 += 64 * kSortUnroll) {
     int64_t tok[kSortUnroll];
 #pragma unroll
@@ -335,7 +353,15 @@ __global__ __launch_bounds__(kSortBlock) void token_sort_kernel(const void* toke
     for (int u = 0; u < kSortUnroll; ++u) {
       const uint64_t r = (uint64_t)tok[u] - v0;  // wraps for a token below v0
       low += tok[u] >= 0 && (uint64_t)tok[u] < v0;
-      if (tok[u] >= 0 && r < rows) atomicAdd(&mine[r], 1u);
+      const bool in = tok[u] >= 0 && r < rows;
+      const uint64_t m = __ballot(in);
+      if (!m) continue;
+      const uint32_t k = listed + __popcll(m & below);
+      if (in) {
+        atomicAdd(&mine[r], 1u);
+        if (k < kSortList) list[wave][k] = (uint32_t)(t0 + u * 64 + lane - begin) << kSortMaxShift | (uint32_t)r;
+      }
+      listed += __popcll(m);
     }
   }
 #pragma unroll
@@ -359,6 +385,8 @@ __global__ __launch_bounds__(kSortBlock) void token_sort_kernel(const void* toke
     for (uint32_t w = 0; w < wave; ++w) at += wave_sum[w];
     uint32_t* o = off + g * (vocab + 1) + v0;
     if (tid < rows) o[tid] = at;
+    first[tid] = at;
+    count[tid] = total;
     if (v0 + rows == vocab && tid == rows - 1) o[rows] = at + total;
     for (int w = 0; w < kSortWaves; ++w) {
       const uint32_t c = cnt[(w << shift) + tid];
@@ -367,6 +395,29 @@ __global__ __launch_bounds__(kSortBlock) void token_sort_kernel(const void* toke
     }
   }
   __syncthreads();
+  // 64 matches in order of position: `in` marks those that are there
+  auto place = [&](bool in, uint32_t r, uint32_t t) {
+    uint64_t same = __ballot(in);
+    for (uint32_t b = 0; b < shift; ++b) {
+      const bool bit = r >> b & 1;
+      const uint64_t m = __ballot(bit);
+      same &= bit ? m : ~m;
+    }
+    // this lane's place among its token's lanes; the first of them counts
+    const uint32_t before = __popcll(same & below);
+    uint32_t at = 0;
+    if (in && before == 0) at = atomicAdd(&mine[r], (uint32_t)__popcll(same));
+    at = __shfl(at, in ? __ffsll((unsigned long long)same) - 1 : 0);
+    if (in) gmem<Place>(order)[g * n_tokens + at + before] = Place{t, (uint32_t)v0 + r, count[r], first[r]};
+  };
+  if (listed <= kSortList && per <= kSortMaxPart) {
+    for (uint32_t k = lane; k - lane < listed; k += 64) {
+      const bool in = k < listed;
+      const uint32_t e = in ? list[wave][k] : 0;
+      place(in, e & ((1u << kSortMaxShift) - 1), (uint32_t)begin + (e >> kSortMaxShift));
+    }
+    return;
+  }
   for (uint64_t t0 = begin; t0 < end; t0 += 64 * kSortUnroll) {
     int64_t tok[kSortUnroll];
 #pragma unroll
@@ -376,23 +427,9 @@ __global__ __launch_bounds__(kSortBlock) void token_sort_kernel(const void* toke
     }
 #pragma unroll
     for (int u = 0; u < kSortUnroll; ++u) {
-      const uint64_t r64 = (uint64_t)tok[u] - v0;
-      const bool in = tok[u] >= 0 && r64 < rows;
-      uint64_t same = __ballot(in);
-      if (!same) continue;
-      const uint32_t r = (uint32_t)r64;
-      for (uint32_t b = 0; b < shift; ++b) {
-        const bool bit = r >> b & 1;
-        const uint64_t m = __ballot(bit);
-        same &= bit ? m : ~m;
-      }
-      // this lane's place among its token's lanes; the first of them counts
-      const uint32_t before = __popcll(same & ((uint64_t(1) << lane) - 1));
-      uint32_t at = 0;
-      if (in && before == 0) at = atomicAdd(&mine[r], (uint32_t)__popcll(same));
-      at = __shfl(at, in ? __ffsll((unsigned long long)same) - 1 : 0);
-      if (in)
-        gmem<Place>(order)[g * n_tokens + at + before] = Place{(uint32_t)(t0 + u * 64 + lane), (uint32_t)tok[u]};
+      const uint64_t r = (uint64_t)tok[u] - v0;
+      const bool in = tok[u] >= 0 && r < rows;
+      if (__ballot(in)) place(in, (uint32_t)r, (uint32_t)(t0 + u * 64 + lane));
     }
   }
 }
@@ -408,28 +445,120 @@ __device__ __forceinline__ RankView rank_view(const fsdp::EmbedGradArgs& a, uint
   return RankView{gmem<uint32_t>(a.off) + g * (a.vocab + 1), gmem<Place>(a.order) + g * a.n_tokens, g * a.n_tokens};
 }
 
-constexpr int kCols = 4;  // columns of a lane in the summing kernels: 16-byte fp32 stores
+constexpr int kGradBlock = 256;
+constexpr int kMinLanes = 16;
+constexpr int kFillBlock = 256, kFillUnroll = 4;
+constexpr uint32_t kFillRun = 16;
+constexpr uint32_t kAhead = 2;
+constexpr uint32_t kWindow = fsdp::kMaxPiece + fsdp::kLong;  // positions that a piece may walk
 
-// sum over sorted positions [b, e) of columns [c, c + 4) of dout, ascending
-template <int D, bool DROP>
-__device__ __forceinline__ void sum_positions(const fsdp::EmbedGradArgs& a, const RankView& rv, const Rng& rng,
-                                              uint32_t b, uint32_t e, uint64_t c, uint32_t len, float (&acc)[kCols]) {
-  constexpr uint32_t kAhead = 8;  // rows in flight
-  for (uint32_t k = b; k < e; k += kAhead) {
-    float v[kAhead][kCols];
-    uint64_t row[kAhead];
+struct GradGrid {
+  uint32_t col_blocks;  // workgroups of pieces side by side along a row
+  uint32_t lanes;       // per piece: 16 to 256, a power of two
+  uint32_t fill_groups, fill_recip;
+};
+
+// The rows without a position, written as zeros (not when the gradient is
+// added to).
+__global__ __launch_bounds__(kFillBlock) void embedding_fill_kernel(fsdp::EmbedGradArgs a, fsdp::RankPtrs grads, uint32_t rank0,
+                                          GradGrid grid) {
+  const RankView rv = rank_view(a, rank0 + blockIdx.y);
+  void* grad = grads.p[blockIdx.y];
+  constexpr uint32_t kItems = kFillBlock * kFillUnroll;
+  const uint64_t first = (uint64_t)xcd_order<kFillRun>(blockIdx.x, gridDim.x) * kItems;
+  const uint64_t n = a.vocab * grid.fill_groups;
+  const Split sp = split_of(first, grid.fill_groups, grid.fill_recip);
+  const uint64_t row_bytes = a.cols * (a.grad_dtype == FSDP_F32 ? 4 : 2);
+  uint64_t v[kFillUnroll];
+  uint32_t j[kFillUnroll], used[kFillUnroll];
+#pragma unroll
+  for (int u = 0; u < kFillUnroll; ++u) {
+    const uint32_t i = u * kFillBlock + threadIdx.x;
+    sp.at(i, v[u], j[u]);
+    used[u] = 1;
+    if (first + i < n) used[u] = rv.off[v[u] + 1] - rv.off[v[u]];
+  }
+#pragma unroll
+  for (int u = 0; u < kFillUnroll; ++u) {
+    if (used[u]) continue;
+    const uint64_t at = v[u] * row_bytes + (uint64_t)j[u] * 16, left = row_bytes - (uint64_t)j[u] * 16;
+    GMEM char* p = gmem<char>(grad) + at;
+    if (left >= 16) {
+      *reinterpret_cast<GMEM u32x4e*>(p) = u32x4{0, 0, 0, 0};
+    } else {
+      for (uint64_t b = 0; b < left; b += 2) *reinterpret_cast<GMEM uint16_t*>(p + b) = 0;
+    }
+  }
+}
+
+constexpr int kCols = 4;  // columns of a lane where rows are summed: 16-byte fp32 stores
+
+// The rows with a position.  a.piece sorted positions at a time: a group of
+// grid.lanes lanes (4 columns a lane) walks them with kAhead rows in flight
+// and puts a token's sum where its positions end.  A token with at most kLong
+// positions belongs to the piece that it begins in, whole; one with more is
+// summed piece by piece into `part` (slot 0: the piece's first token, slot 1:
+// another, which then reaches past its end).
+template <int D, bool DROP, bool ADD>
+__global__ __launch_bounds__(kGradBlock) void embedding_grad_kernel(fsdp::EmbedGradArgs a, fsdp::RankPtrs grads,
+                                                                    uint32_t rank0, GradGrid grid) {
+  __shared__ Place window[kGradBlock / kMinLanes][kWindow];
+  const uint64_t g = rank0 + blockIdx.y;
+  const RankView rv = rank_view(a, g);
+  void* grad = grads.p[blockIdx.y];
+  const uint32_t block = blockIdx.x / grid.col_blocks, col_block = blockIdx.x - block * grid.col_blocks;
+  const uint32_t sub = threadIdx.x / grid.lanes, l = threadIdx.x % grid.lanes;
+  const uint64_t piece = (uint64_t)block * (kGradBlock / grid.lanes) + sub;
+  const uint64_t k0 = piece * a.piece;
+  const uint32_t valid = rv.off[a.vocab];
+  for (uint32_t i = l; i < kWindow; i += grid.lanes)
+    if (k0 + i < a.n_tokens) window[sub][i] = rv.order[k0 + i];
+  __syncthreads();
+  const uint64_t c = ((uint64_t)col_block * grid.lanes + l) * kCols;
+  if (k0 >= valid || c >= a.cols) return;
+  const Place* w = window[sub];
+  const uint32_t len = a.cols - c < kCols ? (uint32_t)(a.cols - c) : kCols;
+  // the positions of this piece, as indices into the window
+  uint32_t k = 0, end = valid - k0 < a.piece ? (uint32_t)(valid - k0) : a.piece;
+  const Place head = w[0], tail = w[end - 1];
+  if (head[3] != k0 && head[2] <= fsdp::kLong) k = head[3] + head[2] - (uint32_t)k0;  // another piece's token
+  if (tail[2] <= fsdp::kLong) end = tail[3] + tail[2] - (uint32_t)k0;
+  const uint64_t pieces = (a.n_tokens + a.piece - 1) / a.piece;
+  float* part = a.part + (g * pieces + piece) * 2 * a.cols;
+  Rng rng;
+  if constexpr (DROP) rng = rng_of(a.drop);
+  float acc[kCols] = {};
+  for (; k < end; k += kAhead) {
+    float v[kAhead][kCols], old[ADD ? kAhead : 1][kCols];
 #pragma unroll
     for (uint32_t u = 0; u < kAhead; ++u)
-      if (k + u < e) {
-        row[u] = rv.row0 + rv.order[k + u][0];
-        load_cols<D, kCols>(a.dout, row[u] * a.cols + c, len, v[u]);
+      if (k + u < end) {
+        const Place p = w[k + u];
+        load_cols<D, kCols>(a.dout, (rv.row0 + p[0]) * a.cols + c, len, v[u]);
+        if constexpr (ADD)  // the old gradient of a token that ends here
+          if (p[2] <= fsdp::kLong && p[3] + p[2] == (uint32_t)k0 + k + u + 1)
+            load_any<kCols>(a.grad_dtype, grad, p[1] * a.cols + c, len, old[u]);
       }
 #pragma unroll
     for (uint32_t u = 0; u < kAhead; ++u)
-      if (k + u < e) {
-        if constexpr (DROP) drop_cols<kCols>(rng, (uint32_t)row[u], (uint32_t)(c / kGroup), c & 4, v[u]);
+      if (k + u < end) {
+        const Place p = w[k + u];
+        if constexpr (DROP)
+          drop_cols<kCols>(rng, (uint32_t)(rv.row0 + p[0]), (uint32_t)(c / kGroup), c & 4, v[u]);
 #pragma unroll
         for (int i = 0; i < kCols; ++i) acc[i] += v[u][i];
+        const bool last = p[3] + p[2] == (uint32_t)k0 + k + u + 1;
+        if (last || k + u + 1 == end) {
+          if (p[2] <= fsdp::kLong) {
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) acc[i] = ADD ? old[ADD ? u : 0][i] + a.factor * acc[i] : a.factor * acc[i];
+            store_any<kCols>(a.grad_dtype, grad, p[1] * a.cols + c, len, acc);
+          } else {
+            store_cols<FSDP_F32, kCols>(part, (p[1] == head[1] ? 0 : a.cols) + c, len, acc);
+          }
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
+        }
       }
   }
 }
@@ -449,101 +578,6 @@ __device__ __forceinline__ void put_grad(const fsdp::EmbedGradArgs& a, void* gra
   store_any<kCols>(a.grad_dtype, grad, v * a.cols + c, len, out);
 }
 
-// Three kinds of workgroups of one launch, the ones with the longest chains of
-// loads first:
-//   pieces  tokens with more than kLong positions, kPiece sorted positions at
-//           a time, into `part` (slot 0: the piece's first token, slot 1: its
-//           last, where that is another)
-//   rows    (sorted position, 4 columns) items: a position that is its
-//           token's first sums the token's whole row, unless it is a long one
-//   fill    the rows without a position, written as zeros (not when the
-//           gradient is added to): 16 bytes a lane and step
-constexpr int kGradBlock = 256;
-constexpr int kFillUnroll = 8;
-
-struct GradGrid {
-  uint32_t pieces, piece_cols;  // workgroups, of them per piece
-  uint32_t rows, groups, recip;
-  uint32_t fill_groups, fill_recip;
-};
-
-template <int D, bool DROP>
-__global__ __launch_bounds__(kGradBlock) void embedding_grad_kernel(fsdp::EmbedGradArgs a, fsdp::RankPtrs grads,
-                                                                    uint32_t rank0, GradGrid grid) {
-  const uint64_t g = rank0 + blockIdx.y;
-  const RankView rv = rank_view(a, g);
-  if (blockIdx.x >= grid.pieces + grid.rows) {
-    constexpr uint32_t kItems = kGradBlock * kFillUnroll;
-    const uint64_t first = (uint64_t)(blockIdx.x - grid.pieces - grid.rows) * kItems;
-    const uint64_t n = a.vocab * grid.fill_groups;
-    const Split sp = split_of(first, grid.fill_groups, grid.fill_recip);
-    const uint32_t es = a.grad_dtype == FSDP_F32 ? 4 : 2;
-    const uint64_t row_bytes = a.cols * es;
-    uint64_t v[kFillUnroll];
-    uint32_t j[kFillUnroll], used[kFillUnroll];
-#pragma unroll
-    for (int u = 0; u < kFillUnroll; ++u) {
-      const uint32_t i = u * kGradBlock + threadIdx.x;
-      sp.at(i, v[u], j[u]);
-      used[u] = 1;
-      if (first + i < n) used[u] = rv.off[v[u] + 1] - rv.off[v[u]];
-    }
-#pragma unroll
-    for (int u = 0; u < kFillUnroll; ++u) {
-      if (used[u]) continue;
-      const uint64_t at = v[u] * row_bytes + (uint64_t)j[u] * 16, left = row_bytes - (uint64_t)j[u] * 16;
-      if (left >= 16) {
-        *reinterpret_cast<GMEM u32x4e*>(gmem<char>(grads.p[blockIdx.y]) + at) = u32x4{0, 0, 0, 0};
-      } else {
-        for (uint64_t b = 0; b < left; b += 2) *reinterpret_cast<GMEM uint16_t*>(gmem<char>(grads.p[blockIdx.y]) + at + b) = 0;
-      }
-    }
-    return;
-  }
-  Rng rng;
-  if constexpr (DROP) rng = rng_of(a.drop);
-  const uint32_t valid = rv.off[a.vocab];
-  if (blockIdx.x >= grid.pieces) {
-    const uint64_t first = (uint64_t)(blockIdx.x - grid.pieces) * kGradBlock;
-    const Split sp = split_of(first, grid.groups, grid.recip);
-    uint64_t at;
-    uint32_t j;
-    sp.at(threadIdx.x, at, j);
-    if (at >= valid) return;
-    const uint32_t v = rv.order[at][1];
-    if (at && rv.order[at - 1][1] == v) return;
-    const uint32_t e = rv.off[(uint64_t)v + 1];
-    if (e - (uint32_t)at > fsdp::kLong) return;
-    const uint64_t c = (uint64_t)j * kCols;
-    const uint32_t len = a.cols - c < kCols ? (uint32_t)(a.cols - c) : kCols;
-    float acc[kCols] = {};
-    sum_positions<D, DROP>(a, rv, rng, (uint32_t)at, e, c, len, acc);
-    put_grad(a, grads.p[blockIdx.y], v, c, len, acc);
-    return;
-  }
-  const uint32_t piece = blockIdx.x / grid.piece_cols;
-  const uint64_t c = ((uint64_t)(blockIdx.x - piece * grid.piece_cols) * kGradBlock + threadIdx.x) * kCols;
-  const uint32_t k0 = piece * fsdp::kPiece;
-  if (k0 >= valid || c >= a.cols) return;
-  const uint32_t k1 = valid - k0 < fsdp::kPiece ? valid : k0 + fsdp::kPiece;
-  const uint32_t len = a.cols - c < kCols ? (uint32_t)(a.cols - c) : kCols;
-  const uint64_t pieces = (a.n_tokens + fsdp::kPiece - 1) / fsdp::kPiece;
-  float* part = a.part + (g * pieces + piece) * 2 * a.cols;
-  const uint64_t va = rv.order[k0][1], vb = rv.order[k1 - 1][1];
-  const uint32_t ea = rv.off[va + 1];
-  if (ea - rv.off[va] > fsdp::kLong) {
-    float acc[kCols] = {};
-    sum_positions<D, DROP>(a, rv, rng, k0, ea < k1 ? ea : k1, c, len, acc);
-    store_cols<FSDP_F32, kCols>(part, c, len, acc);
-  }
-  const uint32_t bb = rv.off[vb];
-  if (vb != va && rv.off[vb + 1] - bb > fsdp::kLong) {
-    float acc[kCols] = {};
-    sum_positions<D, DROP>(a, rv, rng, bb, k1, c, len, acc);
-    store_cols<FSDP_F32, kCols>(part + a.cols, c, len, acc);
-  }
-}
-
 // Joins the pieces of the tokens with more than kLong positions.  Such a
 // token reaches past the piece it begins in, so it is that piece's last one:
 // the workgroups of the piece (64 lanes x 4 columns each) add its partial
@@ -557,14 +591,15 @@ __global__ __launch_bounds__(256) void embedding_join_kernel(fsdp::EmbedGradArgs
   const uint32_t piece = blockIdx.x / col_blocks;
   const uint64_t c = ((uint64_t)(blockIdx.x - piece * col_blocks) * 64 + lane) * kCols;
   const uint32_t valid = rv.off[a.vocab];
-  const uint32_t k0 = piece * fsdp::kPiece;
+  const uint32_t k0 = piece * a.piece;
   if (k0 >= valid) return;
-  const uint32_t k1 = valid - k0 < fsdp::kPiece ? valid : k0 + fsdp::kPiece;
-  const uint64_t v = rv.order[k1 - 1][1];
-  const uint32_t b = rv.off[v], e = rv.off[v + 1];
+  const uint32_t k1 = valid - k0 < a.piece ? valid : k0 + a.piece;
+  const Place tail = rv.order[k1 - 1];
+  const uint64_t v = tail[1];
+  const uint32_t b = tail[3], e = tail[3] + tail[2];
   if (e - b <= fsdp::kLong || b < k0) return;  // the same for the whole workgroup
-  const uint32_t last = (e - 1) / fsdp::kPiece;
-  const uint64_t pieces = (a.n_tokens + fsdp::kPiece - 1) / fsdp::kPiece;
+  const uint32_t last = (e - 1) / a.piece;
+  const uint64_t pieces = (a.n_tokens + a.piece - 1) / a.piece;
   const float* part = a.part + g * pieces * 2 * a.cols;
   const uint32_t len = c >= a.cols ? 0 : a.cols - c < kCols ? (uint32_t)(a.cols - c) : kCols;
   float acc[kCols] = {};
@@ -1102,63 +1137,69 @@ int norm_grad_go(const Launch& go, const fsdp::NormGradArgs& a) {
   return go(norm_grad_wide_kernel<D, false>, grid, 1024, true, false, a, groups);
 }
 
-// Tokens per workgroup of the sort: as few as keep all workgroups of the call
-// resident at once (two of 1024 lanes per CU), at least 16.
+// Tokens per workgroup of the sort: as few as keep the call's workgroups at
+// about one per CU, 16 to 512 (every workgroup reads all tokens: with more
+// of them L2 gets busy, with fewer the one that holds the commonest tokens
+// takes longer).
 uint32_t sort_shift(uint64_t vocab, int n_ranks) {
   uint32_t s = 4;
-  while (s < kSortMaxShift && (vocab * (uint64_t)n_ranks) >> s > 512) ++s;
+  while (s < kSortMaxShift && (vocab * (uint64_t)n_ranks) >> s > 384) ++s;
   return s;
 }
 
 // The workgroups of a gradient call, per rank.
 struct GradPlan {
-  uint32_t shift;
-  uint64_t sort, pieces, piece_cols, rows, fill, join_cols;
+  uint32_t shift, lanes;
+  uint64_t sort, pieces, col_blocks, piece_blocks, fill, join_cols;
 };
 
 GradPlan grad_plan(uint64_t n_tokens, uint64_t vocab, uint64_t cols, int n_ranks, uint64_t grad_bytes, bool accumulate) {
   GradPlan p;
   p.shift = sort_shift(vocab, n_ranks);
   p.sort = ceil_div(vocab, uint64_t(1) << p.shift);
-  p.piece_cols = ceil_div(cols, kGradBlock * kCols);
+  p.lanes = kMinLanes;
+  while (p.lanes < kGradBlock && p.lanes * kCols < cols) p.lanes *= 2;
+  p.pieces = ceil_div(n_tokens, fsdp::embedding_grad_piece(n_tokens, cols, n_ranks));
+  p.col_blocks = ceil_div(cols, (uint64_t)p.lanes * kCols);
+  p.piece_blocks = ceil_div(p.pieces, kGradBlock / p.lanes) * p.col_blocks;
+  p.fill = accumulate ? 0 : ceil_div(vocab * ceil_div(cols * grad_bytes, 16), kFillBlock * kFillUnroll);
   p.join_cols = ceil_div(cols, 64 * kCols);
-  p.pieces = n_tokens > fsdp::kLong ? ceil_div(n_tokens, fsdp::kPiece) : 0;  // else no token has as many
-  p.rows = ceil_div(n_tokens * ceil_div(cols, kCols), kGradBlock);
-  p.fill = accumulate ? 0 : ceil_div(vocab * ceil_div(cols * grad_bytes, 16), kGradBlock * kFillUnroll);
   return p;
 }
 
-template <int D, bool DROP>
+template <int D, bool DROP, bool ADD>
 int embedding_grad_go(const Launch& go, const fsdp::EmbedGradArgs& a) {
   const uint64_t es = a.grad_dtype == FSDP_F32 ? 4 : 2;
-  const GradPlan p = grad_plan(a.n_tokens, a.vocab, a.cols, a.n_ranks, es, a.accumulate);
+  const GradPlan p = grad_plan(a.n_tokens, a.vocab, a.cols, a.n_ranks, es, ADD);
   int rc = go(token_sort_kernel, dim3((uint32_t)p.sort, (uint32_t)a.n_ranks), kSortBlock, true, false, a.tokens,
               a.token_bytes, a.n_tokens, a.vocab, p.shift, a.off, reinterpret_cast<Place*>(a.order));
   if (rc) return rc;
-  const uint64_t groups = ceil_div(a.cols, kCols), fill_groups = ceil_div(a.cols * es, 16);
-  const GradGrid grid{(uint32_t)(p.pieces * p.piece_cols), (uint32_t)p.piece_cols, (uint32_t)p.rows, (uint32_t)groups,
-                      recip_of(groups), (uint32_t)fill_groups, recip_of(fill_groups)};
-  const uint32_t blocks = (uint32_t)(p.pieces * p.piece_cols + p.rows + p.fill);
+  const uint64_t fill_groups = ceil_div(a.cols * es, 16);
+  const GradGrid grid{(uint32_t)p.col_blocks, p.lanes, (uint32_t)fill_groups, recip_of(fill_groups)};
+  const bool join = a.n_tokens > fsdp::kLong;  // else no token has as many positions
   for (int g0 = 0; g0 < a.n_ranks; g0 += fsdp::kMaxRankPtrs) {
     const int n = a.n_ranks - g0 < fsdp::kMaxRankPtrs ? a.n_ranks - g0 : fsdp::kMaxRankPtrs;
     const bool end = g0 + n == a.n_ranks;
     fsdp::RankPtrs ptrs = {};
     for (int k = 0; k < n; ++k) ptrs.p[k] = a.grads[g0 + k];
-    rc = go(embedding_grad_kernel<D, DROP>, dim3(blocks, (uint32_t)n), kGradBlock, false, end && !p.pieces, a, ptrs,
-            (uint32_t)g0, grid);
-    if (rc) return rc;
-    if (p.pieces) {
+    if (!ADD)
+      rc = go(embedding_fill_kernel, dim3((uint32_t)p.fill, (uint32_t)n), kFillBlock, false, end && !p.pieces, a, ptrs,
+              (uint32_t)g0, grid);
+    if (!rc && p.pieces)
+      rc = go(embedding_grad_kernel<D, DROP, ADD>, dim3((uint32_t)p.piece_blocks, (uint32_t)n), kGradBlock, false,
+              end && !join, a, ptrs, (uint32_t)g0, grid);
+    if (!rc && join)
       rc = go(embedding_join_kernel, dim3((uint32_t)(p.pieces * p.join_cols), (uint32_t)n), 256, false, end, a, ptrs,
               (uint32_t)g0, (uint32_t)p.join_cols);
-      if (rc) return rc;
-    }
+    if (rc) return rc;
   }
   return 0;
 }
 
 template <int D>
 int embedding_grad_drop(const Launch& go, const fsdp::EmbedGradArgs& a) {
-  return a.drop.state ? embedding_grad_go<D, true>(go, a) : embedding_grad_go<D, false>(go, a);
+  if (a.accumulate) return a.drop.state ? embedding_grad_go<D, true, true>(go, a) : embedding_grad_go<D, false, true>(go, a);
+  return a.drop.state ? embedding_grad_go<D, true, false>(go, a) : embedding_grad_go<D, false, false>(go, a);
 }
 
 }  // namespace
@@ -1171,6 +1212,13 @@ int fsdp::norm_grad_blocks(uint64_t rows, uint64_t cols, int n_ranks) {
   return (int)(need < 1 ? 1 : need < most ? need : most);
 }
 
+uint32_t fsdp::embedding_grad_piece(uint64_t n_tokens, uint64_t cols, int n_ranks) {
+  const uint64_t waves = ceil_div(cols, 64 * kCols) * (uint64_t)n_ranks;  // per piece
+  uint32_t piece = kMaxPiece;
+  while (piece > kMinPiece && ceil_div(n_tokens, piece) * waves < 8192) piece /= 2;
+  return piece;
+}
+
 // The largest grid: HIP counts a dimension's threads in 32 bits.
 bool fsdp::grid_fits(uint64_t blocks, uint32_t block) { return blocks <= 0xFFFFFFFFull / block; }
 
@@ -1180,7 +1228,7 @@ bool fsdp::embedding_fits(uint64_t n_tokens, uint64_t cols) {
 
 bool fsdp::embedding_grad_fits(uint64_t n_tokens, uint64_t vocab, uint64_t cols, int n_ranks) {
   const GradPlan p = grad_plan(n_tokens, vocab, cols, n_ranks, 4, false);
-  return grid_fits(p.sort, kSortBlock) && grid_fits(p.pieces * p.piece_cols + p.rows + p.fill, kGradBlock) &&
+  return grid_fits(p.sort, kSortBlock) && grid_fits(p.piece_blocks, kGradBlock) && grid_fits(p.fill, kFillBlock) &&
          grid_fits(p.pieces * p.join_cols, 256);
 }
 

@@ -138,10 +138,11 @@ int grad_workspace(int32_t n_ranks, int64_t n_tokens, int64_t vocab, int64_t col
       (rc = check_count(n_tokens, 0, "n_tokens")))
     return rc;
   const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-  const int64_t pieces = n_tokens > fsdp::kLong ? (n_tokens + fsdp::kPiece - 1) / fsdp::kPiece : 0;
+  const int64_t piece = fsdp::embedding_grad_piece(n_tokens, cols, n_ranks);
+  const int64_t pieces = n_tokens > fsdp::kLong ? (n_tokens + piece - 1) / piece : 0;
   int64_t part;
   w->order_at = up(4 * (vocab + 1) * n_ranks);
-  w->part_at = w->order_at + up(8 * n_tokens * n_ranks);
+  w->part_at = w->order_at + up(16 * n_tokens * n_ranks);
   if (!mul_ok(pieces * 8, cols, &part) || !mul_ok(part, n_ranks, &part) || !add_ok(w->part_at, part, &w->bytes))
     return fail(FSDP_EINVAL, "workspace size overflow");
   return FSDP_OK;
@@ -195,6 +196,7 @@ int embedding_grad_impl(int32_t n_ranks, int64_t vocab, int64_t cols, int32_t dt
   a.n_tokens = n_tokens;
   a.vocab = vocab;
   a.cols = cols;
+  a.piece = fsdp::embedding_grad_piece(n_tokens, cols, n_ranks);
   a.factor = (float)(scale * keep);
   a.n_ranks = n_ranks;
   a.dtype = dtype;

@@ -182,9 +182,9 @@ def test_empty_calls_enqueue_nothing(fn, over):
 
 
 def test_workspace_queries():
-    # offsets, order and (more than 32 tokens) two partial rows per 32 positions, 256-byte aligned blocks
-    assert hp.fsdp_embedding_grad_workspace(1, 32, 100, 8) == 512 + 256
-    assert hp.fsdp_embedding_grad_workspace(2, 65, 100, 8) == 1024 + 1280 + 2 * 3 * 2 * 8 * 4
+    # offsets, order and (more than 32 tokens) two partial rows per piece of 4 to 32 positions, 256-byte aligned blocks
+    assert hp.fsdp_embedding_grad_workspace(1, 32, 100, 8) == 512 + 512
+    assert hp.fsdp_embedding_grad_workspace(2, 65, 100, 8) == 1024 + 2304 + 2 * 17 * 2 * 8 * 4
     assert hp.fsdp_norm_grad_workspace(1, 0, 8) == 2 * 8 * 4
     assert hp.fsdp_norm_grad_workspace(8, 1 << 20, 4096) % (8 * 2 * 4096 * 4) == 0
     for call in (lambda: hp.fsdp_embedding_grad_workspace(0, 1, 1, 1), lambda: hp.fsdp_norm_grad_workspace(1, 1, 0),
