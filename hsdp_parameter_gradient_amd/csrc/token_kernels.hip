@@ -458,17 +458,27 @@ struct GradGrid {
   uint32_t fill_groups, fill_recip;
 };
 
+// 16 bytes of zeros at block j of row v of a gradient (fewer at a row's end)
+__device__ __forceinline__ void zero_block(const fsdp::EmbedGradArgs& a, void* grad, uint64_t v, uint32_t j) {
+  const uint64_t row_bytes = a.cols * (a.grad_dtype == FSDP_F32 ? 4 : 2);
+  const uint64_t at = v * row_bytes + (uint64_t)j * 16, left = row_bytes - (uint64_t)j * 16;
+  GMEM char* p = gmem<char>(grad) + at;
+  if (left >= 16) {
+    *reinterpret_cast<GMEM u32x4e*>(p) = u32x4{0, 0, 0, 0};
+  } else {
+    for (uint64_t b = 0; b < left; b += 2) *reinterpret_cast<GMEM uint16_t*>(p + b) = 0;
+  }
+}
+
 // The rows without a position, written as zeros (not when the gradient is
 // added to).
 __global__ __launch_bounds__(kFillBlock) void embedding_fill_kernel(fsdp::EmbedGradArgs a, fsdp::RankPtrs grads, uint32_t rank0,
                                           GradGrid grid) {
   const RankView rv = rank_view(a, rank0 + blockIdx.y);
-  void* grad = grads.p[blockIdx.y];
   constexpr uint32_t kItems = kFillBlock * kFillUnroll;
   const uint64_t first = (uint64_t)xcd_order<kFillRun>(blockIdx.x, gridDim.x) * kItems;
   const uint64_t n = a.vocab * grid.fill_groups;
   const Split sp = split_of(first, grid.fill_groups, grid.fill_recip);
-  const uint64_t row_bytes = a.cols * (a.grad_dtype == FSDP_F32 ? 4 : 2);
   uint64_t v[kFillUnroll];
   uint32_t j[kFillUnroll], used[kFillUnroll];
 #pragma unroll
@@ -480,14 +490,7 @@ __global__ __launch_bounds__(kFillBlock) void embedding_fill_kernel(fsdp::EmbedG
   }
 #pragma unroll
   for (int u = 0; u < kFillUnroll; ++u) {
-    if (used[u]) continue;
-    const uint64_t at = v[u] * row_bytes + (uint64_t)j[u] * 16, left = row_bytes - (uint64_t)j[u] * 16;
-    GMEM char* p = gmem<char>(grad) + at;
-    if (left >= 16) {
-      *reinterpret_cast<GMEM u32x4e*>(p) = u32x4{0, 0, 0, 0};
-    } else {
-      for (uint64_t b = 0; b < left; b += 2) *reinterpret_cast<GMEM uint16_t*>(p + b) = 0;
-    }
+    if (!used[u]) zero_block(a, grads.p[blockIdx.y], v[u], j[u]);
   }
 }
 
@@ -579,51 +582,159 @@ __device__ __forceinline__ void put_grad(const fsdp::EmbedGradArgs& a, void* gra
 }
 
 // Joins the pieces of the tokens with more than kLong positions.  Such a
-// token reaches past the piece it begins in, so it is that piece's last one:
-// the workgroups of the piece (64 lanes x 4 columns each) add its partial
-// sums, every fourth to a wave, and the four waves' sums in a fixed order.
-__global__ __launch_bounds__(256) void embedding_join_kernel(fsdp::EmbedGradArgs a, fsdp::RankPtrs grads,
-                                                             uint32_t rank0, uint32_t col_blocks) {
-  __shared__ float sums[4][64 * kCols];
+// token reaches past the piece it begins in, so it is that piece's last one.
+// A workgroup looks at the last tokens of the pieces of kJoinSpan sorted
+// positions and takes the ones that begin there, one after the other, 256
+// columns of them: its 16 waves add every sixteenth partial sum each, then the
+// waves' sums in a fixed order.
+constexpr int kJoinBlock = 1024;
+constexpr int kJoinSums = kJoinBlock / 64;
+constexpr uint32_t kJoinSpan = 128;
+static_assert(kJoinSpan >= fsdp::kMaxPiece && kJoinSpan / fsdp::kMinPiece <= 64, "one lane per piece");
+
+__global__ __launch_bounds__(kJoinBlock) void embedding_join_kernel(fsdp::EmbedGradArgs a, fsdp::RankPtrs grads,
+                                                                    uint32_t rank0, uint32_t col_blocks) {
+  __shared__ f32x4 sums[kJoinSums][64];
   const uint64_t g = rank0 + blockIdx.y;
   const RankView rv = rank_view(a, g);
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t piece = blockIdx.x / col_blocks;
-  const uint64_t c = ((uint64_t)(blockIdx.x - piece * col_blocks) * 64 + lane) * kCols;
-  const uint32_t valid = rv.off[a.vocab];
-  const uint32_t k0 = piece * a.piece;
-  if (k0 >= valid) return;
-  const uint32_t k1 = valid - k0 < a.piece ? valid : k0 + a.piece;
-  const Place tail = rv.order[k1 - 1];
-  const uint64_t v = tail[1];
-  const uint32_t b = tail[3], e = tail[3] + tail[2];
-  if (e - b <= fsdp::kLong || b < k0) return;  // the same for the whole workgroup
-  const uint32_t last = (e - 1) / a.piece;
+  const uint32_t block = blockIdx.x / col_blocks;
+  const uint64_t c = ((uint64_t)(blockIdx.x - block * col_blocks) * 64 + lane) * kCols;
+  const uint32_t len = c >= a.cols ? 0 : a.cols - c < kCols ? (uint32_t)(a.cols - c) : kCols;
   const uint64_t pieces = (a.n_tokens + a.piece - 1) / a.piece;
   const float* part = a.part + g * pieces * 2 * a.cols;
+  // every wave sees the same: lane i the last position of piece i
+  const uint32_t valid = rv.off[a.vocab];
+  const uint32_t n = kJoinSpan / a.piece;
+  const uint64_t k0 = ((uint64_t)block * n + lane) * a.piece;
+  Place tail{0, 0, 0, 0};
+  if (lane < n && k0 < valid) tail = rv.order[valid - k0 < a.piece ? valid - 1 : k0 + a.piece - 1];
+  uint64_t todo = __ballot(tail[2] > fsdp::kLong && tail[3] >= k0);
+  for (bool again = false; todo; todo &= todo - 1, again = true) {
+    const int i = __ffsll((unsigned long long)todo) - 1;
+    const uint64_t v = (uint32_t)__shfl(tail[1], i);
+    const uint32_t b = __shfl(tail[3], i), e = b + __shfl(tail[2], i);
+    const uint32_t piece = b / a.piece, last = (e - 1) / a.piece;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (len) {
+#pragma unroll 4
+      for (uint32_t q = piece + wave; q <= last; q += kJoinSums) {
+        float p[kCols];
+        const uint64_t slot = 2 * (uint64_t)q + (q == piece && b > piece * a.piece);
+        load_cols<FSDP_F32, kCols>(part, slot * a.cols + c, len, p);
+        acc += f32x4{p[0], p[1], p[2], p[3]};
+      }
+    }
+    if (again) __syncthreads();  // the first wave has read the sums of the token before
+    sums[wave][lane] = acc;
+    __syncthreads();
+    if (wave == 0 && len) {
+      acc = sums[0][lane];
+#pragma unroll
+      for (int w = 1; w < kJoinSums; ++w) acc += sums[w][lane];
+      const float t[kCols] = {acc[0], acc[1], acc[2], acc[3]};
+      put_grad(a, grads.p[blockIdx.y], v, c, len, t);
+    }
+  }
+}
+
+// The gradient of few tokens (at most kSmall per rank) in one launch, without
+// a sort.  A workgroup per position and 1024 columns compares its token with
+// all others: the first position of a token has the ordered list of its
+// matches and sums the row, `lanes` lanes side by side along it, every group
+// of as many lanes taking its share of the matches in turn, the groups' sums
+// added in a fixed order.  Where the gradient is not added to, further
+// workgroups fill the rows that no token names.
+constexpr uint32_t kSmall = 512;
+constexpr int kSmallBlock = 1024;
+constexpr uint32_t kSmallAhead = 4;  // matches in flight
+constexpr uint32_t kSmallRun = 16;
+// When it is taken, measured on MI355X with the calls' host side (us, this
+// kernel / the sorting ones; tokens drawn by 1 / rank, "half" with one token
+// on half of the positions), gradients added to, bf16 into fp32:
+//   1 rank, 512 x 1024      9.4 / 17.0, half 18 / 18
+//   1 rank, 256 x 4096      9.8 / 16.6, half 11 / 17
+//   4 ranks, 256 x 1024     9.9 / 17.5, half 30 / 20
+//   1 rank, 512 x 4096     14.0 / 19.7, half 23 / 19   (beyond kSmallWork)
+//   4 ranks, 512 x 1024    14.0 / 24.2, half 56 / 26   (beyond)
+//   8 ranks, 512 x 64      24.3 / 23.5
+// and written, over 32001 rows: 1 rank, 512 x 1024 28 / 47; 8 ranks, 64 x
+// 4096 649 / 628 (4.2 GB of gradients, beyond kSmallFill: its workgroups look
+// at the tokens once more for every 16 KiB filled).
+constexpr uint64_t kSmallWork = 4096;  // positions times ranks times 256-column blocks
+constexpr uint64_t kSmallFill = uint64_t(1) << 31;  // bytes of all ranks' gradients
+
+template <int D, bool DROP, bool ADD>
+__global__ __launch_bounds__(kSmallBlock) void embedding_grad_small_kernel(fsdp::EmbedGradArgs a, fsdp::RankPtrs grads,
+                                                                           uint32_t rank0, GradGrid grid) {
+  constexpr uint32_t kParts = kSmall / 64;
+  __shared__ uint32_t hit[kSmallBlock];  // a token's positions; or per row: is it named
+  __shared__ uint32_t count[kParts];
+  __shared__ f32x4 sums[kSmallBlock];
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint64_t g = rank0 + blockIdx.y;
+  const uint32_t n = (uint32_t)a.n_tokens;
+  void* grad = grads.p[blockIdx.y];
+  const int64_t tok = tid < n ? token_at(a.tokens, g * n + tid, a.token_bytes) : -1;
+  if (!ADD && blockIdx.x >= n * grid.col_blocks) {
+    const uint32_t b = blockIdx.x - n * grid.col_blocks;
+    const uint64_t first = (uint64_t)xcd_order<kSmallRun>(b, gridDim.x - n * grid.col_blocks) * kSmallBlock;
+    const Split sp = split_of(first, grid.fill_groups, grid.fill_recip);
+    hit[tid] = 0;
+    __syncthreads();
+    if (tok >= 0 && (uint64_t)tok - sp.row0 < kSmallBlock) hit[(uint64_t)tok - sp.row0] = 1;
+    __syncthreads();
+    uint64_t v;
+    uint32_t j;
+    sp.at(tid, v, j);
+    if (first + tid < a.vocab * grid.fill_groups && !hit[v - sp.row0]) zero_block(a, grad, v, j);
+    return;
+  }
+  const uint32_t position = blockIdx.x / grid.col_blocks;
+  const int64_t mine = token_at(a.tokens, g * n + position, a.token_bytes);
+  if (mine < 0 || (uint64_t)mine >= a.vocab) return;
+  const uint64_t m = __ballot(tok == mine);  // positions beyond n hold -1
+  if (wave < kParts && lane == 0) count[wave] = __popcll(m);
+  __syncthreads();
+  uint32_t total = 0;
+#pragma unroll
+  for (uint32_t q = 0; q < kParts; ++q) {
+    if (q == wave && (m >> lane & 1)) hit[total + __popcll(m & ((uint64_t(1) << lane) - 1))] = tid;
+    total += count[q];
+  }
+  __syncthreads();
+  if (hit[0] != position) return;  // not the token's first position
+  Rng rng;
+  if constexpr (DROP) rng = rng_of(a.drop);
+  const uint32_t l = tid % grid.lanes, sub = tid / grid.lanes, groups = kSmallBlock / grid.lanes;
+  const uint64_t c = ((uint64_t)(blockIdx.x - position * grid.col_blocks) * grid.lanes + l) * kCols;
   const uint32_t len = c >= a.cols ? 0 : a.cols - c < kCols ? (uint32_t)(a.cols - c) : kCols;
   float acc[kCols] = {};
   if (len) {
-#pragma unroll 8
-    for (uint32_t q = piece + wave; q <= last; q += 4) {
-      float p[kCols];
-      const uint64_t slot = 2 * (uint64_t)q + (q == piece && b > k0);
-      load_cols<FSDP_F32, kCols>(part, slot * a.cols + c, len, p);
+    for (uint32_t i = sub; i < total; i += groups * kSmallAhead) {
+      float v[kSmallAhead][kCols];
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) acc[i] += p[i];
+      for (uint32_t u = 0; u < kSmallAhead; ++u)
+        if (i + u * groups < total) load_cols<D, kCols>(a.dout, (g * n + hit[i + u * groups]) * a.cols + c, len, v[u]);
+#pragma unroll
+      for (uint32_t u = 0; u < kSmallAhead; ++u)
+        if (i + u * groups < total) {
+          if constexpr (DROP)
+            drop_cols<kCols>(rng, (uint32_t)(g * n + hit[i + u * groups]), (uint32_t)(c / kGroup), c & 4, v[u]);
+#pragma unroll
+          for (int q = 0; q < kCols; ++q) acc[q] += v[u][q];
+        }
     }
   }
+  if (total > 1) {  // the same for the whole workgroup
+    sums[tid] = f32x4{acc[0], acc[1], acc[2], acc[3]};
+    __syncthreads();
+    if (sub == 0)
+      for (uint32_t q = 1; q < (total < groups ? total : groups); ++q)
 #pragma unroll
-  for (int i = 0; i < kCols; ++i) sums[wave][lane * kCols + i] = acc[i];
-  __syncthreads();
-  if (wave == 0 && len) {
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) {
-      const uint32_t s = lane * kCols + i;
-      acc[i] = (sums[0][s] + sums[1][s]) + (sums[2][s] + sums[3][s]);
-    }
-    put_grad(a, grads.p[blockIdx.y], v, c, len, acc);
+        for (int i = 0; i < kCols; ++i) acc[i] += sums[q * grid.lanes + l][i];
   }
+  if (sub == 0 && len) put_grad(a, grad, (uint64_t)mine, c, len, acc);
 }
 
 // --- sums over a row ------------------------------------------------------------
@@ -1150,7 +1261,8 @@ uint32_t sort_shift(uint64_t vocab, int n_ranks) {
 // The workgroups of a gradient call, per rank.
 struct GradPlan {
   uint32_t shift, lanes;
-  uint64_t sort, pieces, col_blocks, piece_blocks, fill, join_cols;
+  uint64_t sort, pieces, col_blocks, piece_blocks, fill, join_cols, join_blocks;
+  uint64_t small;  // of embedding_grad_small_kernel, or 0: the other kernels
 };
 
 GradPlan grad_plan(uint64_t n_tokens, uint64_t vocab, uint64_t cols, int n_ranks, uint64_t grad_bytes, bool accumulate) {
@@ -1164,6 +1276,12 @@ GradPlan grad_plan(uint64_t n_tokens, uint64_t vocab, uint64_t cols, int n_ranks
   p.piece_blocks = ceil_div(p.pieces, kGradBlock / p.lanes) * p.col_blocks;
   p.fill = accumulate ? 0 : ceil_div(vocab * ceil_div(cols * grad_bytes, 16), kFillBlock * kFillUnroll);
   p.join_cols = ceil_div(cols, 64 * kCols);
+  p.join_blocks = ceil_div(n_tokens, kJoinSpan) * p.join_cols;
+  const uint64_t sums = n_tokens * p.col_blocks;
+  p.small = 0;
+  if (n_tokens && n_tokens <= kSmall && n_tokens * n_ranks * ceil_div(cols, 256) <= kSmallWork &&
+      (accumulate || vocab * cols * grad_bytes * n_ranks < kSmallFill))
+    p.small = sums + (accumulate ? 0 : ceil_div(vocab * ceil_div(cols * grad_bytes, 16), kSmallBlock));
   return p;
 }
 
@@ -1171,11 +1289,22 @@ template <int D, bool DROP, bool ADD>
 int embedding_grad_go(const Launch& go, const fsdp::EmbedGradArgs& a) {
   const uint64_t es = a.grad_dtype == FSDP_F32 ? 4 : 2;
   const GradPlan p = grad_plan(a.n_tokens, a.vocab, a.cols, a.n_ranks, es, ADD);
+  const uint64_t groups = ceil_div(a.cols * es, 16);
+  const GradGrid grid{(uint32_t)p.col_blocks, p.lanes, (uint32_t)groups, recip_of(groups)};
+  if (p.small) {
+    for (int g0 = 0; g0 < a.n_ranks; g0 += fsdp::kMaxRankPtrs) {
+      const int n = a.n_ranks - g0 < fsdp::kMaxRankPtrs ? a.n_ranks - g0 : fsdp::kMaxRankPtrs;
+      fsdp::RankPtrs ptrs = {};
+      for (int k = 0; k < n; ++k) ptrs.p[k] = a.grads[g0 + k];
+      const int rc = go(embedding_grad_small_kernel<D, DROP, ADD>, dim3((uint32_t)p.small, (uint32_t)n), kSmallBlock, g0 == 0,
+                        g0 + n == a.n_ranks, a, ptrs, (uint32_t)g0, grid);
+      if (rc) return rc;
+    }
+    return 0;
+  }
   int rc = go(token_sort_kernel, dim3((uint32_t)p.sort, (uint32_t)a.n_ranks), kSortBlock, true, false, a.tokens,
               a.token_bytes, a.n_tokens, a.vocab, p.shift, a.off, reinterpret_cast<Place*>(a.order));
   if (rc) return rc;
-  const uint64_t fill_groups = ceil_div(a.cols * es, 16);
-  const GradGrid grid{(uint32_t)p.col_blocks, p.lanes, (uint32_t)fill_groups, recip_of(fill_groups)};
   const bool join = a.n_tokens > fsdp::kLong;  // else no token has as many positions
   for (int g0 = 0; g0 < a.n_ranks; g0 += fsdp::kMaxRankPtrs) {
     const int n = a.n_ranks - g0 < fsdp::kMaxRankPtrs ? a.n_ranks - g0 : fsdp::kMaxRankPtrs;
@@ -1189,7 +1318,7 @@ int embedding_grad_go(const Launch& go, const fsdp::EmbedGradArgs& a) {
       rc = go(embedding_grad_kernel<D, DROP, ADD>, dim3((uint32_t)p.piece_blocks, (uint32_t)n), kGradBlock, false,
               end && !join, a, ptrs, (uint32_t)g0, grid);
     if (!rc && join)
-      rc = go(embedding_join_kernel, dim3((uint32_t)(p.pieces * p.join_cols), (uint32_t)n), 256, false, end, a, ptrs,
+      rc = go(embedding_join_kernel, dim3((uint32_t)p.join_blocks, (uint32_t)n), kJoinBlock, false, end, a, ptrs,
               (uint32_t)g0, (uint32_t)p.join_cols);
     if (rc) return rc;
   }
@@ -1228,8 +1357,8 @@ bool fsdp::embedding_fits(uint64_t n_tokens, uint64_t cols) {
 
 bool fsdp::embedding_grad_fits(uint64_t n_tokens, uint64_t vocab, uint64_t cols, int n_ranks) {
   const GradPlan p = grad_plan(n_tokens, vocab, cols, n_ranks, 4, false);
-  return grid_fits(p.sort, kSortBlock) && grid_fits(p.piece_blocks, kGradBlock) && grid_fits(p.fill, kFillBlock) &&
-         grid_fits(p.pieces * p.join_cols, 256);
+  return grid_fits(p.sort, kSortBlock) && grid_fits(p.piece_blocks, kGradBlock) && grid_fits(p.fill, kFillBlock) && grid_fits(p.small, kSmallBlock) &&
+         grid_fits(p.join_blocks, kJoinBlock);
 }
 
 int fsdp_launch_embedding(const fsdp::EmbedArgs& a, void* stream, void* start_event, void* stop_event) {

@@ -15,7 +15,8 @@ call (prepare) keeps its own, so it must not overlap in time with itself.
 from __future__ import annotations
 
 import ctypes
-from ctypes import c_int64, c_void_p
+from ctypes import c_int64
+from functools import lru_cache
 from typing import Optional, Sequence
 
 import torch
@@ -25,6 +26,35 @@ from . import _binding as B
 LAYER = "layer"
 RMS = "rms"
 _KINDS = {LAYER: 0, RMS: 1}
+_CODE = B._DTYPES
+_F32 = torch.float32
+
+
+def _ptr(t: torch.Tensor, what: str, numel: int, dtype: Optional[torch.dtype], device: int) -> Optional[int]:
+    """The address of a buffer that a kernel will read or write (None if it is
+    empty), after the checks of _binding._dev and that it is on `device`.
+    These calls are short: the checks that pass cost as little as they can."""
+    try:
+        if t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype) and t.numel() == numel and \
+                t.get_device() == device:
+            return t.data_ptr() if numel else None
+    except AttributeError:
+        pass
+    B._dev(t, what, numel, dtype)
+    raise ValueError(f"{what}: on device {t.get_device()}, the call's other buffers on device {device}")
+
+
+def _device(t: torch.Tensor, what: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: must be a device tensor")
+    return t.get_device()
+
+
+def _code(dtype: torch.dtype) -> int:
+    code = _CODE.get(dtype)
+    return B._dtype_code(dtype) if code is None else code
 
 
 class Dropout:
@@ -37,7 +67,7 @@ class Dropout:
     site: tells the dropouts of one step apart.  The gradient of a call takes
     the Dropout that the call took, with the same seed and step."""
 
-    __slots__ = ("p", "state", "site", "struct", "ref")
+    __slots__ = ("p", "state", "site", "device", "struct", "ref")
 
     def __init__(self, p: float, state: torch.Tensor, site: int = 0):
         if not 0.0 <= p < 1.0 or int(p * 65536 + 0.5) == 65536:
@@ -46,7 +76,16 @@ class Dropout:
             raise ValueError(f"dropout site {site}: expected 32 bits")
         self.p, self.state, self.site = p, state, site
         self.struct = B._Dropout(p, site, B._dev(state, "dropout state", 2, torch.int64))
+        self.device = state.get_device()
         self.ref = ctypes.byref(self.struct)
+
+
+def _drop(d: Optional[Dropout], device: int):
+    if d is None:
+        return None
+    if d.device != device:
+        raise ValueError(f"dropout state: on device {d.device}, the call's other buffers on device {device}")
+    return d.ref
 
 
 def _tokens(tokens: torch.Tensor) -> int:
@@ -56,69 +95,59 @@ def _tokens(tokens: torch.Tensor) -> int:
     return tokens.dtype.itemsize
 
 
-def _opt(t: Optional[torch.Tensor], what: str, numel: int, dtype: torch.dtype) -> Optional[int]:
-    return None if t is None else B._dev(t, what, numel, dtype) or None
-
-
-def _grads(grads: Sequence[torch.Tensor], what: str, n_ranks: int, numel: int, dtype: torch.dtype):
+def _grads(grads: Sequence[torch.Tensor], what: str, n_ranks: int, numel: int, dtype: torch.dtype, device: int):
     if len(grads) != n_ranks:
         raise ValueError(f"{what}: {len(grads)} tensors, expected {n_ranks}")
-    return B._ptr_array([B._dev(t, f"{what}[{g}]", numel, dtype) for g, t in enumerate(grads)])
+    return (ctypes.c_void_p * n_ranks)(*[_ptr(t, what, numel, dtype, device) for t in grads])
 
 
-def _prep_embedding(tokens, table, out, scale=1.0, dropout=None):
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError("table: expected a [vocab, cols] tensor")
-    V, E = table.shape
-    nb, T = _tokens(tokens), tokens.numel()
-    args = (V, E, B._dtype_code(table.dtype), B._dtype_code(out.dtype), B._dev(table, "table", V * E) or None, T, nb,
-            B._dev(tokens, "tokens", T) or None, scale, dropout.ref if dropout is not None else None,
-            B._dev(out, "out", T * E) or None)
-    return B._Call("fsdp_embedding", args, (tokens, table, out, dropout.state if dropout is not None else None, dropout))
+def _issue(name: str, args: tuple, device: int, stream) -> None:
+    """The call on a stream of `device` (default: its current one)."""
+    st = B._stream(stream, device)
+    fn = getattr(B.lib(), name)
+    if torch.cuda.current_device() == device:
+        rc = fn(*args, st)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, st)
+    if rc:
+        B._check(name, rc)
 
 
-class _WorkspaceCall(B._Call):
-    """A marshalled call whose workspace is still to be allocated: at[0] is
-    the workspace's place among the arguments, nbytes its size."""
+def _workspace(nbytes: int, device: int, stream) -> torch.Tensor:
+    """A workspace for a launch on `stream`, from that stream's share of
+    torch's memory: given back after the launch was issued, it goes to later
+    work of the same stream only."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=_torch_device(device))
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=_torch_device(device)) if int(stream) else \
+            torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=_torch_device(device))
 
-    def __init__(self, name, args, keep, at, nbytes):
+
+@lru_cache(maxsize=None)
+def _torch_device(index: int) -> torch.device:
+    return torch.device("cuda", index)
+
+
+class _Prepared(B._Call):
+    """A marshalled call that owns its workspace, if it has one (`at`: its
+    place among the arguments)."""
+
+    def __init__(self, name: str, args: tuple, keep: tuple, at: Optional[int] = None, nbytes: int = 0):
         super().__init__(name, args, keep)
-        self.at, self.nbytes, self.workspace = at, nbytes, None
-
-    def allocate(self, stream=None):
-        """Allocate the workspace for a launch on `stream` (default: the
-        current one), from that stream's share of torch's memory."""
-        if stream is None:
-            ws = torch.empty(self.nbytes, dtype=torch.uint8, device=torch.device("cuda", self.device))
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", self.device)) if int(stream) else \
-                    torch.cuda.default_stream(self.device)
-            with torch.cuda.stream(stream):
-                ws = torch.empty(self.nbytes, dtype=torch.uint8, device=torch.device("cuda", self.device))
-        self.workspace = ws
-        a = list(self.args)
-        a[self.at] = ws.data_ptr()
-        self.args = tuple(a)
-
-    def keep_workspace(self):
-        """For prepared calls: a workspace that lives as long as the call and
-        serves whatever stream the call is issued on (what used its memory
-        before has ended)."""
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError(f"{self.name}: prepare the call before the capture (its workspace outlives the graph)")
-        self.workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=torch.device("cuda", self.device))
-        torch.cuda.current_stream(self.device).synchronize()
-        a = list(self.args)
-        a[self.at] = self.workspace.data_ptr()
-        self.args = tuple(a)
-        return self
-
-    def once(self, stream):
-        self.allocate(stream)
-        self(stream)
+        if at is not None:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError(f"{name}: prepare the call before the capture (its workspace outlives the graph)")
+            self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=_torch_device(self.device))
+            # the call may be issued on any stream: what used this memory before has ended
+            torch.cuda.current_stream(self.device).synchronize()
+            self.args = args[:at] + (self.workspace.data_ptr(),) + args[at + 1:]
 
 
+@lru_cache(maxsize=4096)
 def fsdp_embedding_grad_workspace(n_ranks: int, n_tokens: int, vocab: int, cols: int) -> int:
     """Bytes of fsdp_embedding_grad's workspace (n_tokens of one rank)."""
     n = c_int64()
@@ -127,6 +156,7 @@ def fsdp_embedding_grad_workspace(n_ranks: int, n_tokens: int, vocab: int, cols:
     return n.value
 
 
+@lru_cache(maxsize=4096)
 def fsdp_norm_grad_workspace(n_ranks: int, rows: int, cols: int) -> int:
     """Bytes of fsdp_norm_grad's workspace (rows of one rank)."""
     n = c_int64()
@@ -134,7 +164,21 @@ def fsdp_norm_grad_workspace(n_ranks: int, rows: int, cols: int) -> int:
     return n.value
 
 
-def _marshal_embedding_grad(tokens, dout, grads, scale=1.0, dropout=None, accumulate=False):
+# --- marshalling: (arguments, device), workspaces left out ---------------------
+
+def _embedding(tokens, table, out, scale, dropout):
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table: expected a [vocab, cols] tensor")
+    V, E = table.shape
+    nb, T, dev = _tokens(tokens), tokens.numel(), _device(table, "table")
+    return (V, E, _code(table.dtype), _code(out.dtype), _ptr(table, "table", V * E, None, dev), T, nb,
+            _ptr(tokens, "tokens", T, None, dev), scale, _drop(dropout, dev), _ptr(out, "out", T * E, None, dev)), dev
+
+
+_GRAD_AT = 13  # the workspace among the arguments
+
+
+def _embedding_grad(tokens, dout, grads, scale, dropout, accumulate):
     R = len(grads)
     if R < 1:
         raise ValueError("grads: expected one tensor per rank")
@@ -146,14 +190,12 @@ def _marshal_embedding_grad(tokens, dout, grads, scale=1.0, dropout=None, accumu
     E = dout.shape[-1]
     if E < 1 or grads[0].numel() % E:
         raise ValueError(f"grads[0]: {grads[0].numel()} elements are no rows of {E}")
+    dev = _device(dout, "dout")
     V, T, gd = grads[0].numel() // E, n // R, grads[0].dtype
-    arr = _grads(grads, "grads", R, V * E, gd)
     nbytes = fsdp_embedding_grad_workspace(R, T, V, E)
-    args = (R, V, E, B._dtype_code(dout.dtype), B._dtype_code(gd), T, nb, B._dev(tokens, "tokens", n) or None,
-            B._dev(dout, "dout", n * E) or None, scale, dropout.ref if dropout is not None else None,
-            int(bool(accumulate)), arr, None, nbytes)
-    keep = (tokens, dout, tuple(grads), dropout.state if dropout is not None else None, dropout, arr)
-    return _WorkspaceCall("fsdp_embedding_grad", args, keep, 13, nbytes)
+    return (R, V, E, _code(dout.dtype), _code(gd), T, nb, _ptr(tokens, "tokens", n, None, dev),
+            _ptr(dout, "dout", n * E, None, dev), scale, _drop(dropout, dev), 1 if accumulate else 0,
+            _grads(grads, "grads", R, V * E, gd, dev), None, nbytes), dev
 
 
 def _kind(kind: str) -> int:
@@ -171,53 +213,47 @@ def _rows(x: torch.Tensor, weight: torch.Tensor, what: str):
     return x.numel() // E, E
 
 
-def _prep_norm(x, weight, y, bias=None, residual=None, h=None, mean=None, rstd=None, eps=1e-5, kind=LAYER,
-               dropout=None):
-    k, (n, E), dt, f32 = _kind(kind), _rows(x, weight, "x"), x.dtype, torch.float32
-    args = (k, n, E, B._dtype_code(dt), B._dtype_code(weight.dtype), B._dev(x, "x", n * E) or None,
-            _opt(residual, "residual", n * E, dt), dropout.ref if dropout is not None else None,
-            B._dev(weight, "weight", E), _opt(bias, "bias", E, weight.dtype), eps, _opt(h, "h", n * E, dt),
-            B._dev(y, "y", n * E, dt) or None, _opt(mean, "mean", n, f32), _opt(rstd, "rstd", n, f32))
-    return B._Call("fsdp_norm", args, (x, weight, y, bias, residual, h, mean, rstd,
-                                       dropout.state if dropout is not None else None, dropout))
+def _norm(x, weight, y, bias, residual, h, mean, rstd, eps, kind, dropout):
+    k, (n, E) = _kind(kind), _rows(x, weight, "x")
+    dt, wd, numel, dev = x.dtype, weight.dtype, n * E, _device(x, "x")
+    return (k, n, E, _code(dt), _code(wd), _ptr(x, "x", numel, None, dev),
+            None if residual is None else _ptr(residual, "residual", numel, dt, dev), _drop(dropout, dev),
+            _ptr(weight, "weight", E, None, dev), None if bias is None else _ptr(bias, "bias", E, wd, dev), eps,
+            None if h is None else _ptr(h, "h", numel, dt, dev), _ptr(y, "y", numel, dt, dev),
+            None if mean is None else _ptr(mean, "mean", n, _F32, dev),
+            None if rstd is None else _ptr(rstd, "rstd", n, _F32, dev)), dev
 
 
-def _marshal_norm_grad(dy, h, rstd, weight, dres, dweight, mean=None, dbias=None, dh=None, dx=None, kind=LAYER,
-                       dropout=None, accumulate=False):
-    k, (n, E), dt, f32 = _kind(kind), _rows(dy, weight, "dy"), dy.dtype, torch.float32
+_NORM_AT = 19
+
+
+def _norm_grad(dy, h, rstd, weight, dres, dweight, mean, dbias, dh, dx, kind, dropout, accumulate):
+    k, (n, E) = _kind(kind), _rows(dy, weight, "dy")
     R = len(dweight)
     if R < 1 or n % R:
         raise ValueError(f"dweight: {R} tensors for {n} rows: expected one per rank")
     if mean is None and k == 0:
         raise ValueError("mean: the layer norm's gradient needs it")
-    T, gd = n // R, dweight[0].dtype
-    warr = _grads(dweight, "dweight", R, E, gd)
-    barr = _grads(dbias, "dbias", R, E, gd) if dbias is not None else None
+    dt, numel, T, gd, dev = dy.dtype, n * E, n // R, dweight[0].dtype, _device(dy, "dy")
     nbytes = fsdp_norm_grad_workspace(R, T, E)
-    args = (k, R, T, E, B._dtype_code(dt), B._dtype_code(weight.dtype), B._dtype_code(gd),
-            B._dev(dy, "dy", n * E) or None, _opt(dh, "dh", n * E, dt), B._dev(h, "h", n * E, dt) or None,
-            _opt(mean, "mean", n, f32), B._dev(rstd, "rstd", n, f32) or None, B._dev(weight, "weight", E),
-            dropout.ref if dropout is not None else None, int(bool(accumulate)),
-            B._dev(dres, "dres", n * E, dt) or None, _opt(dx, "dx", n * E, dt), warr, barr, None, nbytes)
-    keep = (dy, h, rstd, weight, dres, tuple(dweight), mean, tuple(dbias or ()), dh, dx,
-            dropout.state if dropout is not None else None, dropout, warr, barr)
-    return _WorkspaceCall("fsdp_norm_grad", args, keep, 19, nbytes)
+    return (k, R, T, E, _code(dt), _code(weight.dtype), _code(gd), _ptr(dy, "dy", numel, None, dev),
+            None if dh is None else _ptr(dh, "dh", numel, dt, dev), _ptr(h, "h", numel, dt, dev),
+            None if mean is None else _ptr(mean, "mean", n, _F32, dev), _ptr(rstd, "rstd", n, _F32, dev),
+            _ptr(weight, "weight", E, None, dev), _drop(dropout, dev), 1 if accumulate else 0,
+            _ptr(dres, "dres", numel, dt, dev), None if dx is None else _ptr(dx, "dx", numel, dt, dev),
+            _grads(dweight, "dweight", R, E, gd, dev),
+            None if dbias is None else _grads(dbias, "dbias", R, E, gd, dev), None, nbytes), dev
 
 
-B._PREP.update({
-    "fsdp_embedding": _prep_embedding,
-    "fsdp_embedding_grad": lambda *a, **k: _marshal_embedding_grad(*a, **k).keep_workspace(),
-    "fsdp_norm": _prep_norm,
-    "fsdp_norm_grad": lambda *a, **k: _marshal_norm_grad(*a, **k).keep_workspace(),
-})
-
+# --- the calls ------------------------------------------------------------------
 
 def fsdp_embedding(tokens: torch.Tensor, table: torch.Tensor, out: torch.Tensor, scale: float = 1.0,
                    dropout: Optional[Dropout] = None, stream=None) -> None:
     """out[t] = drop(scale * table[tokens[t]]); a token outside [0, vocab)
     gives a row of zeros.  table: [vocab, cols]; tokens: int64 or int32, any
     shape; out: [..., cols], its dtype may differ from the table's."""
-    _prep_embedding(tokens, table, out, scale, dropout)(stream)
+    args, dev = _embedding(tokens, table, out, scale, dropout)
+    _issue("fsdp_embedding", args, dev, stream)
 
 
 def fsdp_embedding_grad(tokens: torch.Tensor, dout: torch.Tensor, grads: Sequence[torch.Tensor], scale: float = 1.0,
@@ -225,7 +261,9 @@ def fsdp_embedding_grad(tokens: torch.Tensor, dout: torch.Tensor, grads: Sequenc
     """grads[g][v] = scale * the sum of drop'(dout) over rank g's positions
     with token v (added to grads[g][v] if accumulate).  tokens: the R ranks'
     tokens, R = len(grads), one rank after the other; dout: their rows."""
-    _marshal_embedding_grad(tokens, dout, grads, scale, dropout, accumulate).once(stream)
+    args, dev = _embedding_grad(tokens, dout, grads, scale, dropout, accumulate)
+    ws = _workspace(args[-1], dev, stream)
+    _issue("fsdp_embedding_grad", args[:_GRAD_AT] + (ws.data_ptr(), args[-1]), dev, stream)
 
 
 def fsdp_norm(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -236,7 +274,8 @@ def fsdp_norm(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor, bias: Opti
     last dim (kind RMS: h * rstd * weight, rstd = 1 / rms(h)).  h may be left
     out without a residual and a dropout; mean and rstd (float32, one per row)
     are what the gradient reads."""
-    _prep_norm(x, weight, y, bias, residual, h, mean, rstd, eps, kind, dropout)(stream)
+    args, dev = _norm(x, weight, y, bias, residual, h, mean, rstd, eps, kind, dropout)
+    _issue("fsdp_norm", args, dev, stream)
 
 
 def fsdp_norm_grad(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor, dres: torch.Tensor,
@@ -247,4 +286,34 @@ def fsdp_norm_grad(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight
     """The norm's gradient: dres that of h (and the residual), dh added to it;
     dx that of x (drop'(dres)); dweight[g] and dbias[g] those of rank g's
     rows, R = len(dweight) ranks one after the other."""
-    _marshal_norm_grad(dy, h, rstd, weight, dres, dweight, mean, dbias, dh, dx, kind, dropout, accumulate).once(stream)
+    args, dev = _norm_grad(dy, h, rstd, weight, dres, dweight, mean, dbias, dh, dx, kind, dropout, accumulate)
+    ws = _workspace(args[-1], dev, stream)
+    _issue("fsdp_norm_grad", args[:_NORM_AT] + (ws.data_ptr(), args[-1]), dev, stream)
+
+
+# --- prepared calls (prepare): the signatures of the calls, without the stream ---
+
+def _prep_embedding(tokens, table, out, scale=1.0, dropout=None):
+    return _Prepared("fsdp_embedding", _embedding(tokens, table, out, scale, dropout)[0], (tokens, table, out, dropout))
+
+
+def _prep_embedding_grad(tokens, dout, grads, scale=1.0, dropout=None, accumulate=False):
+    args, _ = _embedding_grad(tokens, dout, grads, scale, dropout, accumulate)
+    return _Prepared("fsdp_embedding_grad", args, (tokens, dout, tuple(grads), dropout), _GRAD_AT, args[-1])
+
+
+def _prep_norm(x, weight, y, bias=None, residual=None, h=None, mean=None, rstd=None, eps=1e-5, kind=LAYER,
+               dropout=None):
+    return _Prepared("fsdp_norm", _norm(x, weight, y, bias, residual, h, mean, rstd, eps, kind, dropout)[0],
+                     (x, weight, y, bias, residual, h, mean, rstd, dropout))
+
+
+def _prep_norm_grad(dy, h, rstd, weight, dres, dweight, mean=None, dbias=None, dh=None, dx=None, kind=LAYER,
+                    dropout=None, accumulate=False):
+    args, _ = _norm_grad(dy, h, rstd, weight, dres, dweight, mean, dbias, dh, dx, kind, dropout, accumulate)
+    return _Prepared("fsdp_norm_grad", args, (dy, h, rstd, weight, dres, tuple(dweight), mean, tuple(dbias or ()), dh,
+                                              dx, dropout), _NORM_AT, args[-1])
+
+
+B._PREP.update({"fsdp_embedding": _prep_embedding, "fsdp_embedding_grad": _prep_embedding_grad,
+                "fsdp_norm": _prep_norm, "fsdp_norm_grad": _prep_norm_grad})

@@ -150,6 +150,14 @@ EGRAD = [  # ranks, tokens, vocab, cols, dout, grad, scale, p, kind, accumulate,
     (70, 9, 6, 10, "f32", "f32", 1.0, 0.0, "outside", False, torch.int64),
     (70, 70, 2, 10, "f32", "bf16", 1.0, 0.0, "one", True, torch.int32),
     (1, 2500, 9, 600, "bf16", "f32", 1.0, 0.5, "one", True, torch.int64),
+    # beyond the sizes of the one-launch kernel
+    (1, 512, 700, 2049, "bf16", "f32", 1.0, 0.0, "padded", False, torch.int64),
+    (3, 513, 513, 7, "f32", "f32", 1.0, 0.25, "skewed", False, torch.int32),
+    (2, 513, 17, 1, "f16", "f16", 1.0, 0.0, "outside", False, torch.int64),
+    (1, 600, 1300, 1027, "bf16", "bf16", 3.0, 0.1, "skewed", True, torch.int64),
+    (8, 900, 33, 130, "bf16", "f32", 1.0, 0.0, "spread", False, torch.int32),
+    (1, 9000, 1500, 12, "f32", "f32", 1.0, 0.0, "one", False, torch.int64),
+    (1, 20000, 300, 20, "f32", "f32", 1.0, 0.0, "skewed", False, torch.int64),
 ]
 
 
