@@ -15,6 +15,18 @@
 #include "fsdp_flat.h"
 #include "token.hpp"
 
+#ifndef NCAP
+#define NCAP 1
+#endif
+#ifndef N1
+#define N1 64, 2
+#endif
+#ifndef N4
+#define N4 512, 1
+#endif
+#ifndef N8
+#define N8 1024, 1
+#endif
 namespace {
 
 #define GMEM __attribute__((address_space(1)))
@@ -133,6 +145,70 @@ __device__ __forceinline__ void store_cols(void* base, uint64_t at, uint32_t n, 
   }
 }
 
+// A group of 8 columns as it is in memory: loads whose values are wanted later
+// hold no more registers than their bytes.
+template <int D>
+struct Raw {
+  u32x4 w[D == FSDP_F32 ? 2 : 1];
+};
+
+template <int D>
+__device__ __forceinline__ Raw<D> load_raw(const void* base, uint64_t at, uint32_t n) {
+  typedef typename Elem<D>::T T;
+  const GMEM T* p = gmem<T>(base) + at;
+  Raw<D> r;
+  if (n >= 8) {
+    r.w[0] = *reinterpret_cast<const GMEM u32x4e*>(p);
+    if constexpr (D == FSDP_F32) r.w[1] = *reinterpret_cast<const GMEM u32x4e*>(p + 4);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const T e = (uint32_t)k < n ? p[k] : T(0);
+      if constexpr (D == FSDP_F32) {
+        r.w[k / 4][k % 4] = __builtin_bit_cast(uint32_t, e);
+      } else {
+        r.w[0][k / 2] = k % 2 ? r.w[0][k / 2] | (uint32_t)e << 16 : (uint32_t)e;
+      }
+    }
+  }
+  return r;
+}
+
+template <int D>
+__device__ __forceinline__ void unpack(const Raw<D>& r, float (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (D == FSDP_F32) {
+      const uint32_t lo = r.w[k / 2][2 * k % 4], hi = r.w[k / 2][2 * k % 4 + 1];
+      v[2 * k] = __builtin_bit_cast(float, lo);
+      v[2 * k + 1] = __builtin_bit_cast(float, hi);
+    } else {
+      unpack2<D>(r.w[0][k], v[2 * k], v[2 * k + 1]);
+    }
+  }
+}
+
+// v rounded to D: stored, and left in v.
+template <int D>
+__device__ __forceinline__ void store_rounded(void* base, uint64_t at, uint32_t n, float (&v)[8]) {
+  if constexpr (D == FSDP_F32) {
+    store_cols<D, 8>(base, at, n, v);
+  } else {
+    Raw<D> r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.w[0][k] = pack2<D>(v[2 * k], v[2 * k + 1]);
+    GMEM uint16_t* p = gmem<uint16_t>(base) + at;
+    if (n >= 8) {
+      *reinterpret_cast<GMEM u32x4e*>(p) = r.w[0];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if ((uint32_t)k < n) p[k] = (uint16_t)(r.w[0][k / 2] >> 16 * (k % 2));
+    }
+    unpack<D>(r, v);
+  }
+}
+
 // The same for a dtype known at run time only (the same for every lane).
 template <int N>
 __device__ __forceinline__ void load_any(int dtype, const void* base, uint64_t at, uint32_t n, float (&v)[N]) {
@@ -196,18 +272,13 @@ __device__ __forceinline__ Rng rng_of(const fsdp::Drop& d) {
 template <int N>
 __device__ __forceinline__ void drop_cols(const Rng& g, uint32_t row, uint32_t group, uint32_t half, float (&v)[N]) {
   const u32x4 w = random_bits(group, row, g.site, g.step, g.k0, g.k1);
-  if constexpr (N == 8) {
+  // a 16-bit lane below cut: compared as the upper half of 32 bits
+  const uint32_t cut = g.cut << 16;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t u = k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu;
-      v[k] = u < g.cut ? 0.0f : v[k];
-    }
-  } else {
-    const uint32_t a = half ? w[2] : w[0], b = half ? w[3] : w[1];
-    v[0] = (a & 0xFFFFu) < g.cut ? 0.0f : v[0];
-    v[1] = (a >> 16) < g.cut ? 0.0f : v[1];
-    v[2] = (b & 0xFFFFu) < g.cut ? 0.0f : v[2];
-    v[3] = (b >> 16) < g.cut ? 0.0f : v[3];
+  for (int k = 0; k < N / 2; ++k) {
+    const uint32_t u = N == 8 ? w[k] : half ? w[k + 2] : w[k];
+    v[2 * k] = u << 16 < cut ? 0.0f : v[2 * k];
+    v[2 * k + 1] = u < cut ? 0.0f : v[2 * k + 1];
   }
 }
 
@@ -739,16 +810,38 @@ __global__ __launch_bounds__(kSmallBlock) void embedding_grad_small_kernel(fsdp:
 
 // --- sums over a row ------------------------------------------------------------
 
+// The sum of x over the 64 lanes of a wave, or over each 16 of them, in every
+// lane: within rows of 16 lanes by cross-lane operands of the additions
+// themselves (no LDS), then the rows' sums by lane reads.
+template <int CTRL>
+__device__ __forceinline__ float add_lanes(float x) {
+  return x + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true));
+}
+
+template <int LANES>
+__device__ __forceinline__ float wave_sum(float x) {
+  x = add_lanes<0xB1>(x);   // lane ^ 1
+  x = add_lanes<0x4E>(x);   // lane ^ 2
+  x = add_lanes<0x141>(x);  // mirrored in 8
+  x = add_lanes<0x140>(x);  // mirrored in 16
+  if constexpr (LANES > 16) {
+    const int i = __builtin_bit_cast(int, x);
+    const float a = __builtin_bit_cast(float, __builtin_amdgcn_readlane(i, 0));
+    const float b = __builtin_bit_cast(float, __builtin_amdgcn_readlane(i, 16));
+    const float c = __builtin_bit_cast(float, __builtin_amdgcn_readlane(i, 32));
+    const float d = __builtin_bit_cast(float, __builtin_amdgcn_readlane(i, 48));
+    x = (a + b) + (c + d);
+  }
+  return x;
+}
+
 // LANES lanes hold one row (16, 64, or a whole workgroup of 256, 512 or 1024):
 // the sums of `a` and `b` over the row, in every one of its lanes.  `slot`
 // alternates between calls, so that one barrier per call is enough.
 template <int LANES>
 __device__ __forceinline__ void row_sum2(float& a, float& b, float (*lds)[2][LANES < 64 ? 1 : LANES / 64], int slot) {
-#pragma unroll
-  for (int s = (LANES < 64 ? LANES : 64) / 2; s; s >>= 1) {
-    a += __shfl_xor(a, s);
-    b += __shfl_xor(b, s);
-  }
+  a = wave_sum<LANES>(a);
+  b = wave_sum<LANES>(b);
   if constexpr (LANES > 64) {
     constexpr int W = LANES / 64;
     if ((threadIdx.x & 63) == 0) {
@@ -769,52 +862,74 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float (*lds)[2][LAN
 
 constexpr int block_of(int lanes) { return lanes < 256 ? 256 : lanes; }
 
+// The columns of group j that exist: 8, fewer in a row's last group, 0 beyond.
+__device__ __forceinline__ uint32_t group_len(uint64_t cols, uint32_t j) {
+  const uint64_t c = (uint64_t)j * kGroup;
+  return c >= cols ? 0 : cols - c < kGroup ? (uint32_t)(cols - c) : kGroup;
+}
+
 // h = residual + drop(x), rounded to the activations' type (the norm and its
 // gradient see the same h); y = (h - mean) * rstd * weight + bias.  LANES
 // lanes keep a row in registers, NV groups each, so that x and the residual
-// are read once.  The variance is the mean square of h - mean, less the
-// square of what rounding the mean left: a row far from zero loses nothing.
+// are read once; they walk down the rows with weight and bias in registers
+// and the next row's loads in flight.  The variance is the mean square of
+// h - mean, less the square of what rounding the mean left: a row far from
+// zero loses nothing.
 template <int D, int LANES, int NV, bool DROP>
-__global__ __launch_bounds__(block_of(LANES)) void norm_kernel(fsdp::NormArgs a, uint32_t groups) {
+__global__ __launch_bounds__(block_of(LANES)) void norm_kernel(fsdp::NormArgs a) {
   constexpr int kRows = block_of(LANES) / LANES;
   __shared__ float lds[2][2][LANES < 64 ? 1 : LANES / 64];
   const uint32_t l = threadIdx.x % LANES;
+  const uint64_t step = (uint64_t)gridDim.x * kRows;
+  uint64_t row = (uint64_t)blockIdx.x * kRows + threadIdx.x / LANES;
+  uint32_t len[NV];
+  float w[NV][8], bias[NV][8] = {};
+  Raw<D> x[NV], res[NV];
+  auto load_row = [&](uint64_t r) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (len[i]) {
+        const uint64_t at = r * a.cols + (uint64_t)(l + i * LANES) * kGroup;
+        x[i] = load_raw<D>(a.x, at, len[i]);
+        if (a.residual) res[i] = load_raw<D>(a.residual, at, len[i]);
+      }
+  };
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    len[i] = group_len(a.cols, l + i * LANES);
+    x[i] = res[i] = Raw<D>{};
+  }
+  if (row < a.rows) load_row(row);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const uint64_t at = (uint64_t)(l + i * LANES) * kGroup;
+    load_any<8>(a.weight_dtype, a.weight, len[i] ? at : 0, len[i], w[i]);
+    if (a.bias) load_any<8>(a.weight_dtype, a.bias, len[i] ? at : 0, len[i], bias[i]);
+  }
   Rng rng;
   if constexpr (DROP) rng = rng_of(a.drop);
   const float inv = 1.0f / (float)a.cols;
   int slot = 0;
-  for (uint64_t row = (uint64_t)blockIdx.x * kRows + threadIdx.x / LANES; row < a.rows;
-       row += (uint64_t)gridDim.x * kRows) {
+  for (; row < a.rows; row += step) {
     float v[NV][8];
-    uint32_t len[NV];
     const uint64_t at = row * a.cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const uint32_t j = l + i * LANES;
-      len[i] = j >= groups ? 0 : a.cols - (uint64_t)j * kGroup < kGroup ? (uint32_t)(a.cols - (uint64_t)j * kGroup) : kGroup;
-      load_cols<D, 8>(a.x, len[i] ? at + (uint64_t)j * kGroup : 0, len[i], v[i]);
-    }
-    if (a.h) {
+      unpack<D>(x[i], v[i]);
+      if constexpr (DROP) drop_cols<8>(rng, (uint32_t)row, j, 0, v[i]);
+      if (a.residual) {
+        float r[8];
+        unpack<D>(res[i], r);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const uint32_t j = l + i * LANES;
-        if (!len[i]) continue;
-        if constexpr (DROP) {
+        for (int k = 0; k < 8; ++k) v[i][k] = DROP ? __builtin_fmaf(v[i][k], a.factor, r[k]) : v[i][k] + r[k];
+      } else if constexpr (DROP) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[i][k] *= a.factor;
-          drop_cols<8>(rng, (uint32_t)row, j, 0, v[i]);
-        }
-        if (a.residual) {
-          float r[8];
-          load_cols<D, 8>(a.residual, at + (uint64_t)j * kGroup, len[i], r);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[i][k] += r[k];
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] = Elem<D>::get(Elem<D>::put(v[i][k]));
-        store_cols<D, 8>(a.h, at + (uint64_t)j * kGroup, len[i], v[i]);
+        for (int k = 0; k < 8; ++k) v[i][k] *= a.factor;
       }
+      if (a.h && len[i]) store_rounded<D>(a.h, at + (uint64_t)j * kGroup, len[i], v[i]);
     }
+    if (row + step < a.rows) load_row(row + step);
     float mean = 0.0f, sum = 0.0f, sq = 0.0f;
     if (!a.rms) {
 #pragma unroll
@@ -825,15 +940,22 @@ __global__ __launch_bounds__(block_of(LANES)) void norm_kernel(fsdp::NormArgs a,
       slot ^= 1;
       mean = sum * inv;
       sum = sq = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (len[i] == kGroup) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[i][k] -= mean;
+        } else {  // absent columns stay zero
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[i][k] = (uint32_t)k < len[i] ? v[i][k] - mean : 0.0f;
+        }
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float d = (uint32_t)k < len[i] ? v[i][k] - mean : 0.0f;
-        v[i][k] = d;
-        sum += d;
-        sq += d * d;
+        sum += v[i][k];
+        sq = __builtin_fmaf(v[i][k], v[i][k], sq);
       }
     row_sum2<LANES>(sum, sq, lds, slot);
     slot ^= 1;
@@ -845,18 +967,9 @@ __global__ __launch_bounds__(block_of(LANES)) void norm_kernel(fsdp::NormArgs a,
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const uint32_t j = l + i * LANES;
-      if (!len[i]) continue;
-      float w[8];
-      load_any<8>(a.weight_dtype, a.weight, (uint64_t)j * kGroup, len[i], w);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[i][k] = (v[i][k] - rest) * rstd * w[k];
-      if (a.bias) {
-        load_any<8>(a.weight_dtype, a.bias, (uint64_t)j * kGroup, len[i], w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] += w[k];
-      }
-      store_cols<D, 8>(a.y, at + (uint64_t)j * kGroup, len[i], v[i]);
+      for (int k = 0; k < 8; ++k) v[i][k] = __builtin_fmaf(v[i][k] - rest, rstd * w[i][k], bias[i][k]);
+      if (len[i]) store_cols<D, 8>(a.y, at + (uint64_t)(l + i * LANES) * kGroup, len[i], v[i]);
     }
   }
 }
@@ -1203,25 +1316,24 @@ int embedding_table(const Launch& go, const fsdp::EmbedArgs& a) {
 }
 
 template <int D, int LANES, int NV>
-int norm_rows(const Launch& go, const fsdp::NormArgs& a, uint32_t groups) {
-  constexpr uint64_t rows = block_of(LANES) / LANES;
-  const uint64_t need = ceil_div(a.rows, rows);
-  const uint64_t cap = 256 * 16;
+int norm_rows(const Launch& go, const fsdp::NormArgs& a) {
+  constexpr int block = block_of(LANES);
+  const uint64_t need = ceil_div(a.rows, block / LANES), cap = NCAP * 256 * (2048 / block);
   const dim3 grid((uint32_t)(need < cap ? need : cap));
-  if (a.drop.state) return go(norm_kernel<D, LANES, NV, true>, grid, block_of(LANES), true, true, a, groups);
-  return go(norm_kernel<D, LANES, NV, false>, grid, block_of(LANES), true, true, a, groups);
+  if (a.drop.state) return go(norm_kernel<D, LANES, NV, true>, grid, block, true, true, a);
+  return go(norm_kernel<D, LANES, NV, false>, grid, block, true, true, a);
 }
 
 template <int D>
 int norm_go(const Launch& go, const fsdp::NormArgs& a) {
   const uint32_t groups = (uint32_t)ceil_div(a.cols, kGroup);
-  if (groups <= 16) return norm_rows<D, 16, 1>(go, a, groups);
-  if (groups <= 64) return norm_rows<D, 64, 1>(go, a, groups);
-  if (groups <= 128) return norm_rows<D, 64, 2>(go, a, groups);
-  if (groups <= 256) return norm_rows<D, 256, 1>(go, a, groups);
-  if (groups <= 512) return norm_rows<D, 256, 2>(go, a, groups);
-  if (groups <= 1024) return norm_rows<D, 512, 2>(go, a, groups);
-  if (groups <= 2048) return norm_rows<D, 1024, 2>(go, a, groups);
+  if (groups <= 16) return norm_rows<D, 16, 1>(go, a);
+  if (groups <= 64) return norm_rows<D, 64, 1>(go, a);
+  if (groups <= 128) return norm_rows<D, N1>(go, a);
+  if (groups <= 256) return norm_rows<D, 256, 1>(go, a);
+  if (groups <= 512) return norm_rows<D, N4>(go, a);
+  if (groups <= 1024) return norm_rows<D, N8>(go, a);
+  if (groups <= 2048) return norm_rows<D, 1024, 2>(go, a);
   const dim3 grid((uint32_t)(a.rows < 1024 ? a.rows : 1024));
   if (a.drop.state) return go(norm_wide_kernel<D, true>, grid, 1024, true, true, a, groups);
   return go(norm_wide_kernel<D, false>, grid, 1024, true, true, a, groups);
