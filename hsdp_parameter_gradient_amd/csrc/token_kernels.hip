@@ -15,18 +15,6 @@
 #include "fsdp_flat.h"
 #include "token.hpp"
 
-#ifndef NCAP
-#define NCAP 1
-#endif
-#ifndef N1
-#define N1 64, 2
-#endif
-#ifndef N4
-#define N4 512, 1
-#endif
-#ifndef N8
-#define N8 1024, 1
-#endif
 namespace {
 
 #define GMEM __attribute__((address_space(1)))
@@ -188,7 +176,8 @@ __device__ __forceinline__ void unpack(const Raw<D>& r, float (&v)[8]) {
   }
 }
 
-// v rounded to D: stored, and left in v.
+// v rounded to D: stored past the caches (h is next read by the backward pass,
+// or behind the sublayer's matrix products), and left in v.
 template <int D>
 __device__ __forceinline__ void store_rounded(void* base, uint64_t at, uint32_t n, float (&v)[8]) {
   if constexpr (D == FSDP_F32) {
@@ -199,7 +188,7 @@ __device__ __forceinline__ void store_rounded(void* base, uint64_t at, uint32_t 
     for (int k = 0; k < 4; ++k) r.w[0][k] = pack2<D>(v[2 * k], v[2 * k + 1]);
     GMEM uint16_t* p = gmem<uint16_t>(base) + at;
     if (n >= 8) {
-      *reinterpret_cast<GMEM u32x4e*>(p) = r.w[0];
+      __builtin_nontemporal_store(r.w[0], reinterpret_cast<GMEM u32x4e*>(p));
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -860,7 +849,8 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float (*lds)[2][LAN
 
 // --- norm -----------------------------------------------------------------------
 
-constexpr int block_of(int lanes) { return lanes < 256 ? 256 : lanes; }
+constexpr uint32_t kNormRun = 64;
+constexpr int block_of(int lanes) { return lanes <= 64 ? 256 : lanes; }
 
 // The columns of group j that exist: 8, fewer in a row's last group, 0 beyond.
 __device__ __forceinline__ uint32_t group_len(uint64_t cols, uint32_t j) {
@@ -881,7 +871,7 @@ __global__ __launch_bounds__(block_of(LANES)) void norm_kernel(fsdp::NormArgs a)
   __shared__ float lds[2][2][LANES < 64 ? 1 : LANES / 64];
   const uint32_t l = threadIdx.x % LANES;
   const uint64_t step = (uint64_t)gridDim.x * kRows;
-  uint64_t row = (uint64_t)blockIdx.x * kRows + threadIdx.x / LANES;
+  uint64_t row = (uint64_t)xcd_order<kNormRun>(blockIdx.x, gridDim.x) * kRows + threadIdx.x / LANES;
   uint32_t len[NV];
   float w[NV][8], bias[NV][8] = {};
   Raw<D> x[NV], res[NV];
@@ -1061,52 +1051,71 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(fsdp::NormArgs a, uint3
 // (rms: without mean(g)), and over a rank's rows dweight = sum dy * xhat,
 // dbias = sum dy.  A lane keeps the same columns in every row, so the two
 // column sums stay in its registers; a workgroup writes them once, as one row
-// of `part`, after its waves' sums were added in LDS in a fixed order.
+// of `part`, after its waves' sums were added in LDS in a fixed order.  The
+// next row's loads are in flight while a row is computed.  Absent columns
+// load as dy = 0 and add nothing.
 template <int D, int LANES, int NV, bool DROP>
-__global__ __launch_bounds__(block_of(LANES)) void norm_grad_kernel(fsdp::NormGradArgs a, uint32_t groups) {
+__global__ __launch_bounds__(block_of(LANES)) void norm_grad_kernel(fsdp::NormGradArgs a) {
   constexpr int kBlockSize = block_of(LANES);
   constexpr int kRows = kBlockSize / LANES;
   constexpr uint32_t kWidth = LANES * NV * kGroup;  // columns the lanes of a row cover
   __shared__ float lds[2][2][LANES < 64 ? 1 : LANES / 64];
   __shared__ float cross[kRows > 1 ? kRows * kWidth : 1];
   const uint32_t l = threadIdx.x % LANES, sub = threadIdx.x / LANES;
-  const uint64_t g = blockIdx.y;
+  const uint64_t g = blockIdx.y, step = (uint64_t)gridDim.x * kRows;
+  uint64_t r = (uint64_t)blockIdx.x * kRows + sub;
+  uint32_t len[NV];
+  Raw<D> h[NV], dy[NV], dh[NV];
+  float mean = 0.0f, rstd = 0.0f;
+  auto load_row = [&](uint64_t row) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (len[i]) {
+        const uint64_t at = row * a.cols + (uint64_t)(l + i * LANES) * kGroup;
+        h[i] = load_raw<D>(a.h, at, len[i]);
+        dy[i] = load_raw<D>(a.dy, at, len[i]);
+        if (a.dh) dh[i] = load_raw<D>(a.dh, at, len[i]);
+      }
+    if (a.mean) mean = gmem<float>(a.mean)[row];
+    rstd = gmem<float>(a.rstd)[row];
+  };
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    len[i] = group_len(a.cols, l + i * LANES);
+    h[i] = dy[i] = dh[i] = Raw<D>{};
+  }
+  if (r < a.rows) load_row(g * a.rows + r);
+  float w[NV][8], dw[NV][8] = {}, db[NV][8] = {};
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    load_any<8>(a.weight_dtype, a.weight, len[i] ? (uint64_t)(l + i * LANES) * kGroup : 0, len[i], w[i]);
   Rng rng;
   if constexpr (DROP) rng = rng_of(a.drop);
   const float inv = 1.0f / (float)a.cols;
-  float w[NV][8], dw[NV][8] = {}, db[NV][8] = {};
-  uint32_t len[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const uint32_t j = l + i * LANES;
-    len[i] = j >= groups ? 0 : a.cols - (uint64_t)j * kGroup < kGroup ? (uint32_t)(a.cols - (uint64_t)j * kGroup) : kGroup;
-    load_any<8>(a.weight_dtype, a.weight, len[i] ? (uint64_t)j * kGroup : 0, len[i], w[i]);
-  }
   int slot = 0;
-  for (uint64_t r = (uint64_t)blockIdx.x * kRows + sub; r < a.rows; r += (uint64_t)gridDim.x * kRows) {
+  for (; r < a.rows; r += step) {
     const uint64_t row = g * a.rows + r, at = row * a.cols;
-    float x[NV][8], dy[NV][8];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const uint64_t p = len[i] ? at + (uint64_t)(l + i * LANES) * kGroup : 0;
-      load_cols<D, 8>(a.h, p, len[i], x[i]);
-      load_cols<D, 8>(a.dy, p, len[i], dy[i]);
-    }
-    const float mean = a.mean ? a.mean[row] : 0.0f, rstd = a.rstd[row];
+    float x[NV][8], gw[NV][8];
     float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      unpack<D>(h[i], x[i]);
+      unpack<D>(dy[i], gw[i]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float xh = (uint32_t)k < len[i] ? (x[i][k] - mean) * rstd : 0.0f;
-        dw[i][k] += dy[i][k] * xh;
-        db[i][k] += dy[i][k];
-        const float gw = dy[i][k] * w[i][k];
-        x[i][k] = xh;
-        dy[i][k] = gw;
-        s0 += gw;
-        s1 += gw * xh;
+        x[i][k] = (x[i][k] - mean) * rstd;
+        dw[i][k] = __builtin_fmaf(gw[i][k], x[i][k], dw[i][k]);
+        db[i][k] += gw[i][k];
+        gw[i][k] *= w[i][k];
+        s0 += gw[i][k];
+        s1 = __builtin_fmaf(gw[i][k], x[i][k], s1);
       }
+    }
+    const float rs = rstd;
+    Raw<D> past[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) past[i] = dh[i];
+    if (r + step < a.rows) load_row(row + step);
     row_sum2<LANES>(s0, s1, lds, slot);
     slot ^= 1;
     const float m0 = a.rms ? 0.0f : s0 * inv, m1 = s1 * inv;
@@ -1115,20 +1124,19 @@ __global__ __launch_bounds__(block_of(LANES)) void norm_grad_kernel(fsdp::NormGr
       if (!len[i]) continue;
       const uint32_t j = l + i * LANES;
       const uint64_t p = at + (uint64_t)j * kGroup;
+      float t[8];
+      unpack<D>(past[i], t);  // zeros without dh
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[i][k] = rstd * ((dy[i][k] - m0) - x[i][k] * m1);
-      if (a.dh) {
-        float t[8];
-        load_cols<D, 8>(a.dh, p, len[i], t);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[i][k] += t[k];
+      for (int k = 0; k < 8; ++k) {
+        const float d = __builtin_fmaf(-m1, x[i][k], gw[i][k] - m0);
+        x[i][k] = __builtin_fmaf(rs, d, t[k]);
       }
       store_cols<D, 8>(a.dres, p, len[i], x[i]);
       if (a.dx) {
         if constexpr (DROP) {
+          drop_cols<8>(rng, (uint32_t)row, j, 0, x[i]);
 #pragma unroll
           for (int k = 0; k < 8; ++k) x[i][k] *= a.factor;
-          drop_cols<8>(rng, (uint32_t)row, j, 0, x[i]);
         }
         store_cols<D, 8>(a.dx, p, len[i], x[i]);
       }
@@ -1315,11 +1323,21 @@ int embedding_table(const Launch& go, const fsdp::EmbedArgs& a) {
   }
 }
 
+// Lanes per row and groups per lane, by the groups of a row, and the most
+// workgroups (in multiples of what fills the chip at 2048 lanes per CU; the
+// rest of the rows go round again).  Measured on MI355X, bf16, residual and h,
+// us (us with another choice):
+//   1024 columns    64 x 2, once    16384 rows  27 (4 times the chip: 32)
+//   2048 columns   256 x 1, 4 times 16384 rows  50 (once: 54)
+//   4096 columns   512 x 1, 4 times 16384 rows  97 (once: 109; 256 x 2: 103),
+//                  256 x 2 without h  53 (512 x 1: 60)
+//   8192 columns  1024 x 1, once     8192 rows  96 (4 times: 99; 512 x 2: 97)
+//  16384 columns  1024 x 2, once     4096 rows  99 (4 times: 108)
 template <int D, int LANES, int NV>
-int norm_rows(const Launch& go, const fsdp::NormArgs& a) {
+int norm_rows(const Launch& go, const fsdp::NormArgs& a, uint64_t times) {
   constexpr int block = block_of(LANES);
-  const uint64_t need = ceil_div(a.rows, block / LANES), cap = NCAP * 256 * (2048 / block);
-  const dim3 grid((uint32_t)(need < cap ? need : cap));
+  const uint64_t need = ceil_div(a.rows, block / LANES), most = times * 256 * (2048 / block);
+  const dim3 grid((uint32_t)(need < most ? need : most));
   if (a.drop.state) return go(norm_kernel<D, LANES, NV, true>, grid, block, true, true, a);
   return go(norm_kernel<D, LANES, NV, false>, grid, block, true, true, a);
 }
@@ -1327,34 +1345,49 @@ int norm_rows(const Launch& go, const fsdp::NormArgs& a) {
 template <int D>
 int norm_go(const Launch& go, const fsdp::NormArgs& a) {
   const uint32_t groups = (uint32_t)ceil_div(a.cols, kGroup);
-  if (groups <= 16) return norm_rows<D, 16, 1>(go, a);
-  if (groups <= 64) return norm_rows<D, 64, 1>(go, a);
-  if (groups <= 128) return norm_rows<D, N1>(go, a);
-  if (groups <= 256) return norm_rows<D, 256, 1>(go, a);
-  if (groups <= 512) return norm_rows<D, N4>(go, a);
-  if (groups <= 1024) return norm_rows<D, N8>(go, a);
-  if (groups <= 2048) return norm_rows<D, 1024, 2>(go, a);
+  if (groups <= 16) return norm_rows<D, 16, 1>(go, a, 1);
+  if (groups <= 64) return norm_rows<D, 64, 1>(go, a, 1);
+  if (groups <= 128) return norm_rows<D, 64, 2>(go, a, 1);
+  if (groups <= 256) return norm_rows<D, 256, 1>(go, a, 4);
+  if (groups <= 512) return a.h ? norm_rows<D, 512, 1>(go, a, 4) : norm_rows<D, 256, 2>(go, a, 4);
+  if (groups <= 1024) return norm_rows<D, 1024, 1>(go, a, 1);
+  if (groups <= 2048) return norm_rows<D, 1024, 2>(go, a, 1);
   const dim3 grid((uint32_t)(a.rows < 1024 ? a.rows : 1024));
   if (a.drop.state) return go(norm_wide_kernel<D, true>, grid, 1024, true, true, a, groups);
   return go(norm_wide_kernel<D, false>, grid, 1024, true, true, a, groups);
 }
 
+#ifndef G1
+#define G1 64, 2
+#endif
+#ifndef G2
+#define G2 256, 1
+#endif
+#ifndef G4
+#define G4 512, 1
+#endif
+#ifndef G8
+#define G8 1024, 1
+#endif
+#ifndef GB
+#define GB 512
+#endif
 template <int D, int LANES, int NV>
-int norm_grad_rows(const Launch& go, const fsdp::NormGradArgs& a, uint32_t groups) {
+int norm_grad_rows(const Launch& go, const fsdp::NormGradArgs& a) {
   const dim3 grid((uint32_t)a.blocks, (uint32_t)a.n_ranks);
-  if (a.drop.state) return go(norm_grad_kernel<D, LANES, NV, true>, grid, block_of(LANES), true, false, a, groups);
-  return go(norm_grad_kernel<D, LANES, NV, false>, grid, block_of(LANES), true, false, a, groups);
+  if (a.drop.state) return go(norm_grad_kernel<D, LANES, NV, true>, grid, block_of(LANES), true, false, a);
+  return go(norm_grad_kernel<D, LANES, NV, false>, grid, block_of(LANES), true, false, a);
 }
 
 template <int D>
 int norm_grad_go(const Launch& go, const fsdp::NormGradArgs& a) {
   const uint32_t groups = (uint32_t)ceil_div(a.cols, kGroup);
-  if (groups <= 16) return norm_grad_rows<D, 16, 1>(go, a, groups);
-  if (groups <= 64) return norm_grad_rows<D, 64, 1>(go, a, groups);
-  if (groups <= 128) return norm_grad_rows<D, 64, 2>(go, a, groups);
-  if (groups <= 256) return norm_grad_rows<D, 256, 1>(go, a, groups);
-  if (groups <= 512) return norm_grad_rows<D, 256, 2>(go, a, groups);
-  if (groups <= 1024) return norm_grad_rows<D, 512, 2>(go, a, groups);
+  if (groups <= 16) return norm_grad_rows<D, 16, 1>(go, a);
+  if (groups <= 64) return norm_grad_rows<D, 64, 1>(go, a);
+  if (groups <= 128) return norm_grad_rows<D, G1>(go, a);
+  if (groups <= 256) return norm_grad_rows<D, G2>(go, a);
+  if (groups <= 512) return norm_grad_rows<D, G4>(go, a);
+  if (groups <= 1024) return norm_grad_rows<D, G8>(go, a);
   const dim3 grid((uint32_t)a.blocks, (uint32_t)a.n_ranks);
   if (a.drop.state) return go(norm_grad_wide_kernel<D, true>, grid, 1024, true, false, a, groups);
   return go(norm_grad_wide_kernel<D, false>, grid, 1024, true, false, a, groups);
@@ -1449,7 +1482,7 @@ int embedding_grad_drop(const Launch& go, const fsdp::EmbedGradArgs& a) {
 // each of a workgroup's rows in flight.
 int fsdp::norm_grad_blocks(uint64_t rows, uint64_t cols, int n_ranks) {
   const uint64_t in_flight = cols <= 128 ? 16 : cols <= 1024 ? 4 : 1;
-  const uint64_t most = ceil_div(512, (uint64_t)n_ranks), need = ceil_div(rows, in_flight);
+  const uint64_t most = ceil_div(GB, (uint64_t)n_ranks), need = ceil_div(rows, in_flight);
   return (int)(need < 1 ? 1 : need < most ? need : most);
 }
 
