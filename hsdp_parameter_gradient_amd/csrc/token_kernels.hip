@@ -110,19 +110,29 @@ __device__ __forceinline__ void load_cols(const void* base, uint64_t at, uint32_
   }
 }
 
-template <int D, int N>
+// PAST: stored past the caches (nontemporal).
+template <int D, int N, bool PAST = false>
 __device__ __forceinline__ void store_cols(void* base, uint64_t at, uint32_t n, const float (&v)[N]) {
   typedef typename Elem<D>::T T;
   GMEM T* p = gmem<T>(base) + at;
   if (n >= N) {
     if constexpr (D == FSDP_F32) {
 #pragma unroll
-      for (int k = 0; k < N; k += 4) *reinterpret_cast<GMEM f32x4e*>(p + k) = f32x4{v[k], v[k + 1], v[k + 2], v[k + 3]};
+      for (int k = 0; k < N; k += 4) {
+        const f32x4 w = {v[k], v[k + 1], v[k + 2], v[k + 3]};
+        if constexpr (PAST)
+          __builtin_nontemporal_store(w, reinterpret_cast<GMEM f32x4e*>(p + k));
+        else
+          *reinterpret_cast<GMEM f32x4e*>(p + k) = w;
+      }
     } else if constexpr (N == 8) {
       u32x4 w;
 #pragma unroll
       for (int k = 0; k < 4; ++k) w[k] = pack2<D>(v[2 * k], v[2 * k + 1]);
-      *reinterpret_cast<GMEM u32x4e*>(p) = w;
+      if constexpr (PAST)
+        __builtin_nontemporal_store(w, reinterpret_cast<GMEM u32x4e*>(p));
+      else
+        *reinterpret_cast<GMEM u32x4e*>(p) = w;
     } else {
       *reinterpret_cast<GMEM u32x2e*>(p) = u32x2{pack2<D>(v[0], v[1]), pack2<D>(v[2], v[3])};
     }
@@ -181,7 +191,7 @@ __device__ __forceinline__ void unpack(const Raw<D>& r, float (&v)[8]) {
 template <int D>
 __device__ __forceinline__ void store_rounded(void* base, uint64_t at, uint32_t n, float (&v)[8]) {
   if constexpr (D == FSDP_F32) {
-    store_cols<D, 8>(base, at, n, v);
+    store_cols<D, 8, true>(base, at, n, v);
   } else {
     Raw<D> r;
 #pragma unroll
@@ -1131,7 +1141,7 @@ __global__ __launch_bounds__(block_of(LANES)) void norm_grad_kernel(fsdp::NormGr
         const float d = __builtin_fmaf(-m1, x[i][k], gw[i][k] - m0);
         x[i][k] = __builtin_fmaf(rs, d, t[k]);
       }
-      store_cols<D, 8>(a.dres, p, len[i], x[i]);
+      store_cols<D, 8, DROP>(a.dres, p, len[i], x[i]);
       if (a.dx) {
         if constexpr (DROP) {
           drop_cols<8>(rng, (uint32_t)row, j, 0, x[i]);
@@ -1260,6 +1270,7 @@ __global__ __launch_bounds__(kJoinWaves * 64) void norm_join_kernel(fsdp::NormGr
   const float* part = a.part + (g * a.blocks * sums + s) * a.cols;
   float t = 0.0f;
   if (c < a.cols)
+#pragma unroll 8
     for (uint32_t b = wave; b < (uint32_t)a.blocks; b += kJoinWaves) t += gmem<float>(part)[(uint64_t)b * sums * a.cols + c];
   lds[wave][lane] = t;
   __syncthreads();
@@ -1357,21 +1368,6 @@ int norm_go(const Launch& go, const fsdp::NormArgs& a) {
   return go(norm_wide_kernel<D, false>, grid, 1024, true, true, a, groups);
 }
 
-#ifndef G1
-#define G1 64, 2
-#endif
-#ifndef G2
-#define G2 256, 1
-#endif
-#ifndef G4
-#define G4 512, 1
-#endif
-#ifndef G8
-#define G8 1024, 1
-#endif
-#ifndef GB
-#define GB 512
-#endif
 template <int D, int LANES, int NV>
 int norm_grad_rows(const Launch& go, const fsdp::NormGradArgs& a) {
   const dim3 grid((uint32_t)a.blocks, (uint32_t)a.n_ranks);
@@ -1384,10 +1380,10 @@ int norm_grad_go(const Launch& go, const fsdp::NormGradArgs& a) {
   const uint32_t groups = (uint32_t)ceil_div(a.cols, kGroup);
   if (groups <= 16) return norm_grad_rows<D, 16, 1>(go, a);
   if (groups <= 64) return norm_grad_rows<D, 64, 1>(go, a);
-  if (groups <= 128) return norm_grad_rows<D, G1>(go, a);
-  if (groups <= 256) return norm_grad_rows<D, G2>(go, a);
-  if (groups <= 512) return norm_grad_rows<D, G4>(go, a);
-  if (groups <= 1024) return norm_grad_rows<D, G8>(go, a);
+  if (groups <= 128) return norm_grad_rows<D, 64, 2>(go, a);
+  if (groups <= 256) return norm_grad_rows<D, 256, 1>(go, a);
+  if (groups <= 512) return norm_grad_rows<D, 512, 1>(go, a);
+  if (groups <= 1024) return norm_grad_rows<D, 1024, 1>(go, a);
   const dim3 grid((uint32_t)a.blocks, (uint32_t)a.n_ranks);
   if (a.drop.state) return go(norm_grad_wide_kernel<D, true>, grid, 1024, true, false, a, groups);
   return go(norm_grad_wide_kernel<D, false>, grid, 1024, true, false, a, groups);
@@ -1478,11 +1474,13 @@ int embedding_grad_drop(const Launch& go, const fsdp::EmbedGradArgs& a) {
 
 }  // namespace
 
-// Enough workgroups to fill the chip over all ranks, and at least one row for
-// each of a workgroup's rows in flight.
+// Workgroups over all ranks, and at least one row for each of a workgroup's
+// rows in flight.  Measured on MI355X, us (us with the other count): 256
+// workgroups 16384 x 4096 103 (512: 116), 8192 x 8192 109 (119); 512
+// workgroups 16384 x 2048 61 (256: 69), 65536 x 256 48 (63).
 int fsdp::norm_grad_blocks(uint64_t rows, uint64_t cols, int n_ranks) {
   const uint64_t in_flight = cols <= 128 ? 16 : cols <= 1024 ? 4 : 1;
-  const uint64_t most = ceil_div(GB, (uint64_t)n_ranks), need = ceil_div(rows, in_flight);
+  const uint64_t most = ceil_div(cols <= 2048 ? 512 : 256, (uint64_t)n_ranks), need = ceil_div(rows, in_flight);
   return (int)(need < 1 ? 1 : need < most ? need : most);
 }
 
