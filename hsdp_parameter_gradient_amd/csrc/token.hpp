@@ -34,6 +34,7 @@ struct EmbedArgs {
   uint64_t n_tokens, vocab, cols;
   float factor;  // scale, times 65536 / (65536 - cut) with a dropout
   int table_dtype, out_dtype, token_bytes;
+  int past;  // store past the caches (set by the launcher)
   Drop drop;
 };
 

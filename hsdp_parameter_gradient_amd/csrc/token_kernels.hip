@@ -330,9 +330,18 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t b, uint32_t n) {
 // --- embedding ------------------------------------------------------------------
 
 // out[t] = drop(factor * table[token[t]]): one pass, bound by reading the
-// rows looked up and writing the output.  A lane moves kEmbedUnroll groups.
-constexpr int kEmbedBlock = 256;
-constexpr int kEmbedUnroll = 4;
+// rows looked up (the common ones from L2 and the MALL) and writing the
+// output.  A lane moves kEmbedUnroll groups.  Measured on MI355X, 16384 x 4096
+// bf16 45 us, 20011 x 1021 fp32 to fp16 with dropout 16 us; 256 lanes x 4
+// groups 48 and 17, 1024 x 1 50 and 16.
+//
+// An output of the MALL's size or more is stored past the caches.  A smaller
+// one is not: its own call gets faster (16384 x 4096: 33 us), but the norm
+// that reads it next loses more (both together 93 -> 96 us, 8192 x 4096 50 ->
+// 55 us; 32768 x 4096 184 -> 181 us).
+constexpr int kEmbedBlock = 512;
+constexpr int kEmbedUnroll = 2;
+constexpr uint64_t kPastBytes = uint64_t(256) << 20;
 
 template <int TD, int OD, bool DROP>
 __global__ __launch_bounds__(kEmbedBlock) void embedding_kernel(fsdp::EmbedArgs a, uint32_t groups, uint32_t recip) {
@@ -364,7 +373,11 @@ __global__ __launch_bounds__(kEmbedBlock) void embedding_kernel(fsdp::EmbedArgs 
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[u][k] *= a.factor;
     if constexpr (DROP) drop_cols<8>(rng, (uint32_t)row[u], grp[u], 0, v[u]);
-    store_cols<OD, 8>(a.out, row[u] * a.cols + (uint64_t)grp[u] * kGroup, len[u], v[u]);
+    const uint64_t at = row[u] * a.cols + (uint64_t)grp[u] * kGroup;
+    if (a.past)
+      store_cols<OD, 8, true>(a.out, at, len[u], v[u]);
+    else
+      store_cols<OD, 8>(a.out, at, len[u], v[u]);
   }
 }
 
@@ -1317,9 +1330,10 @@ Launch launch_of(void* stream, void* start, void* stop) {
 }
 
 template <int TD, int OD>
-int embedding_go(const Launch& go, const fsdp::EmbedArgs& a) {
+int embedding_go(const Launch& go, fsdp::EmbedArgs a) {
   const uint64_t groups = ceil_div(a.cols, kGroup);
   const dim3 grid((uint32_t)ceil_div(a.n_tokens * groups, kEmbedBlock * kEmbedUnroll));
+  a.past = a.n_tokens * a.cols * (OD == FSDP_F32 ? 4 : 2) >= kPastBytes;
   if (a.drop.state)
     return go(embedding_kernel<TD, OD, true>, grid, kEmbedBlock, true, true, a, (uint32_t)groups, recip_of(groups));
   return go(embedding_kernel<TD, OD, false>, grid, kEmbedBlock, true, true, a, (uint32_t)groups, recip_of(groups));

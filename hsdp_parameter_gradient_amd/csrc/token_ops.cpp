@@ -123,6 +123,7 @@ int embedding_impl(int64_t vocab, int64_t cols, int32_t table_dtype, int32_t out
   a.table_dtype = table_dtype;
   a.out_dtype = out_dtype;
   a.token_bytes = token_bytes;
+  a.past = 0;
   const Timing t(stream);
   return launched(fsdp_launch_embedding(a, stream, t.start, t.stop), "embedding");
 }

@@ -18,7 +18,9 @@ of one bucket of parameters with all R simulated ranks resident in HBM:
 and runs the hot path with one library call per step.  Which gradient
 collectives run follows the decision matrix of the FullyShard
 multi-dimensional RFC (sections 2.2.2 and 2.2.5): RS when shard_size > 1,
-AR when dp_size > 1.  The shard views (AG inputs) and the per-rank full
+AR when dp_size > 1.  Between the AG and the RS, embedding(), norm() and their
+gradients work on the bucket's full parameters and write its bound full
+gradients.  The shard views (AG inputs) and the per-rank full
 gradients (RS copy-in inputs) belong to the caller.
 """
 
@@ -29,6 +31,7 @@ from typing import List, Optional, Sequence
 import torch
 
 from . import _binding as B
+from . import token_ops as T
 
 
 class FlatBucket:
@@ -83,6 +86,7 @@ class FlatBucket:
         _, self.ar_numel = B.fsdp_fused_layout([I], grad_dtype.itemsize)
         self.ar_buffers = [f[self.fused_off:self.fused_off + self.ar_numel] for f in self.fused]
         self._calls = None
+        self._grads = None
 
     # -- the caller's inputs ------------------------------------------------
     def shard_views(self, params: Sequence[torch.Tensor]) -> List[torch.Tensor]:
@@ -117,6 +121,7 @@ class FlatBucket:
     def bind(self, shards: Sequence[torch.Tensor], grads: Sequence[torch.Tensor]) -> "FlatBucket":
         """Marshal the five calls once: shards [S*P] rank-major, grads [R*P]."""
         S, R, dims = self.S, self.R, self.shard_dims
+        self._grads = list(grads)
         self._calls = {
             "ag_copy_in": B.prepare("fsdp_ag_copy_in", self.shapes, S, list(shards), self.ag, dims),
             "ag_copy_out": B.prepare("fsdp_ag_copy_out", self.shapes, S, self.ag, self.full, dims),
@@ -138,6 +143,47 @@ class FlatBucket:
         if self.do_ar:
             st.append("fused_ar")
         return st
+
+    # -- what a layer does with the bucket's parameters ---------------------
+    def param(self, i: int) -> torch.Tensor:
+        """Full parameter i, as the operators below read it: the view of the
+        gathered buffer for a one-parameter bucket sharded on dim 0 (valid
+        once the AG has run, no copy-out needed), else full[i]."""
+        if len(self.shapes) == 1 and not (self.shard_dims and self.shard_dims[0] != 0):
+            return self.full_views()[0]
+        return self.full[i]
+
+    def grads(self, i: int) -> List[torch.Tensor]:
+        """The R bound full gradients of parameter i."""
+        if self._grads is None:
+            raise RuntimeError("FlatBucket: call bind(shards, grads) before its parameters' gradients")
+        P = len(self.shapes)
+        return [self._grads[g * P + i] for g in range(self.R)]
+
+    def embedding(self, i: int, tokens: torch.Tensor, out: torch.Tensor, scale: float = 1.0, dropout=None,
+                  stream=None) -> None:
+        """Look all ranks' tokens up in parameter i ([vocab, cols]): see
+        fsdp_embedding."""
+        T.fsdp_embedding(tokens, self.param(i), out, scale, dropout, stream)
+
+    def embedding_grad(self, i: int, tokens: torch.Tensor, dout: torch.Tensor, scale: float = 1.0, dropout=None,
+                       accumulate: bool = False, stream=None) -> None:
+        """Write (or add to) the R bound gradients of parameter i: see
+        fsdp_embedding_grad."""
+        T.fsdp_embedding_grad(tokens, dout, self.grads(i), scale, dropout, accumulate, stream)
+
+    def norm(self, i: int, x: torch.Tensor, y: torch.Tensor, bias: Optional[int] = None, **kwargs) -> None:
+        """The norm with parameter i as its weight and, if given, parameter
+        `bias` as its bias; the other arguments as fsdp_norm's."""
+        T.fsdp_norm(x, self.param(i), y, bias=None if bias is None else self.param(bias), **kwargs)
+
+    def norm_grad(self, i: int, dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, dres: torch.Tensor,
+                  bias: Optional[int] = None, **kwargs) -> None:
+        """The norm's gradient, that of its weight (and bias) into the R bound
+        gradients of parameter i (and `bias`); the other arguments as
+        fsdp_norm_grad's."""
+        T.fsdp_norm_grad(dy, h, rstd, self.param(i), dres, self.grads(i),
+                         dbias=None if bias is None else self.grads(bias), **kwargs)
 
     def _call(self, step: str):
         if self._calls is None:

@@ -20,7 +20,7 @@ All streams keep the default priority.
 
 from __future__ import annotations
 
-from typing import List, Sequence
+from typing import Callable, List, Optional, Sequence
 
 import torch
 
@@ -28,8 +28,18 @@ from .flat_bucket import FlatBucket
 
 
 class BackwardPipeline:
-    def __init__(self, buckets: Sequence[FlatBucket], fused_rs: bool = True):
+    def __init__(self, buckets: Sequence[FlatBucket], fused_rs: bool = True,
+                 backward: Optional[Sequence[Callable[[], None]]] = None):
+        """backward: one callable per bucket that issues the calls writing its
+        bound gradients (embedding_grad, norm_grad, the matrix products) on
+        the current stream; each layer's RS then starts behind its own calls
+        and runs beside the next layer's.  Default: the gradients are there
+        when the pipeline starts.  graph() issues the calls once eagerly
+        before it captures them, so they write rather than accumulate."""
         self.buckets: List[FlatBucket] = list(buckets)
+        self.backward = list(backward) if backward is not None else None
+        if self.backward is not None and len(self.backward) != len(self.buckets):
+            raise ValueError(f"backward: {len(self.backward)} callables for {len(self.buckets)} buckets")
         self.fused_rs = fused_rs
         self.rs_stream = torch.cuda.Stream()
         self.ar_stream = torch.cuda.Stream()
@@ -48,6 +58,9 @@ class BackwardPipeline:
         self.rs_stream.wait_stream(cur)  # gradients and buffers are ready
         self.ar_stream.wait_stream(cur)
         for l, b in enumerate(self.buckets):
+            if self.backward is not None:
+                self.backward[l]()
+                self.rs_stream.wait_stream(cur)
             # step 3: this layer's RS, asynchronously on the shard-domain stream
             self._rs(b, self.rs_stream)
             self._rs_done[l].record(self.rs_stream)
@@ -83,6 +96,8 @@ class BackwardPipeline:
     def run_serial(self) -> None:
         """The same kernels in the same order on the current stream."""
         for l, b in enumerate(self.buckets):
+            if self.backward is not None:
+                self.backward[l]()
             self._rs(b, None)
             if l > 0 and self.buckets[l - 1].do_ar:
                 self.buckets[l - 1].run("fused_ar", None)

@@ -664,3 +664,150 @@ def test_time_next_launch_covers_the_call():
     hp.fsdp_norm_grad(y, x, rstd, w, torch.empty_like(x), [gw], kind=hp.RMS)
     torch.cuda.synchronize()
     assert 0 < start.elapsed_time(stop) < 5
+
+
+# --- the operators in the path of a bucket ---------------------------------------------
+
+class _Layer:
+    """An embedding table (a bucket of its own) and a norm (weight and bias
+    between other parameters), HSDP 4 = 2 x 2, bf16 parameters, fp32 gradients:
+    AG, lookup, norm, their gradients, RS and AR."""
+
+    V, E, n, R, S = 70, 40, 24, 4, 2
+
+    def __init__(self, seed, one_bucket=False):
+        rng = _rng(8, seed)
+        V, E, n, R, S = self.V, self.E, self.n, self.R, self.S
+        self.params = {"table": _values(rng, (V, E), "bf16"), "w": _values(rng, (E,), "bf16", 0.3, 1.0),
+                       "b": _values(rng, (E,), "bf16", 0.3), "other": _values(rng, (5, 3), "bf16")}
+        sets = [["other", "w", "b", "table"]] if one_bucket else [["other", "w", "b"], ["table"]]
+        self.at = {k: (i, j) for i, s in enumerate(sets) for j, k in enumerate(s)}
+        self.buckets, self.grads = [], []
+        for names in sets:
+            shapes = [self.params[k].shape for k in names]
+            fb = hp.FlatBucket(shapes, R, S, torch.bfloat16, op="avg", device="cuda")
+            dev = [torch.from_numpy(self.params[k]).to(torch.bfloat16).cuda() for k in names]
+            grads = [torch.full((int(np.prod(s)),), float("nan"), device="cuda") for _ in range(R) for s in shapes]
+            for g in range(R):  # the parameter that nothing here computes a gradient of
+                if "other" in names:
+                    grads[g * len(names) + names.index("other")].fill_(float(g))
+            self.buckets.append(fb.bind(fb.shard_views(dev), grads))
+        self.tok = torch.from_numpy(_tokens(rng, R * n, V, "outside")).cuda().view(R, n)
+        bf = lambda: torch.from_numpy(_values(rng, (R * n, E), "bf16")).to(torch.bfloat16).cuda()  # noqa: E731
+        self.dy, self.dh, self.res = bf(), bf(), bf()
+        self.x, self.h, self.y, self.dres, self.dx = (torch.empty_like(self.dy) for _ in range(5))
+        self.mean, self.rstd = torch.empty(R * n, device="cuda"), torch.empty(R * n, device="cuda")
+        self.state = _state()
+        self.d0, self.d1 = hp.Dropout(0.1, self.state, 0), hp.Dropout(0.25, self.state, 1)
+        (self.nb, self.wi), (_, self.bi), (self.eb, self.ti) = self.at["w"], self.at["b"], self.at["table"]
+
+    def forward(self):
+        for k, fb in enumerate(self.buckets):
+            fb.run("ag_copy_in")
+            if len(fb.shapes) > 1:  # a one-parameter bucket is read from the gathered buffer
+                fb.run("ag_copy_out")
+            else:
+                fb.full[0].fill_(float("nan"))
+        self.buckets[self.eb].embedding(self.ti, self.tok, self.x, scale=4.0, dropout=self.d0)
+        self.buckets[self.nb].norm(self.wi, self.x, self.y, bias=self.bi, residual=self.res, h=self.h, mean=self.mean,
+                                   rstd=self.rstd, dropout=self.d1)
+
+    def norm_backward(self):
+        self.buckets[self.nb].norm_grad(self.wi, self.dy, self.h, self.rstd, self.dres, bias=self.bi, mean=self.mean,
+                                        dh=self.dh, dx=self.dx, dropout=self.d1)
+
+    def table_backward(self):
+        self.buckets[self.eb].embedding_grad(self.ti, self.tok, self.dx, scale=4.0, dropout=self.d0)
+
+    def check(self):
+        """Every stage against the oracle, given what the stage before it left."""
+        V, E, n, R, S = self.V, self.E, self.n, self.R, self.S
+        fac = [T.dropout_factors(R * n, E, d.p, SEED, STEP, d.site) for d in (self.d0, self.d1)]
+        tok = self.tok.cpu().numpy().reshape(-1)
+        x = T.embedding(tok, self.params["table"], 4.0, fac[0])
+        _close("x", _host(self.x), x, (HALF["bf16"] + 2 * U) * 1.01 * np.abs(x))
+        h, tol = _h_tol(_host(self.x), _host(self.res), fac[1], "bf16")
+        _close("h", _host(self.h), h, tol * 1.01)
+        hv, K = _host(self.h), _depth(E)
+        y, m, r = T.norm(hv, self.params["w"], self.params["b"], 1e-5, False)
+        # h and the parameters are of order 1: y's fp32 errors are below (K + 20) U of 50
+        _close("y", _host(self.y), y, HALF["bf16"] * np.abs(y) * 1.01 + (K + 20) * U * 50)
+        mean, rstd = _host(self.mean), _host(self.rstd)
+        d = T.norm_grad(_host(self.dy), hv, mean, rstd, self.params["w"], _host(self.dh), False)[0]
+        _close("dres", _host(self.dres), d, HALF["bf16"] * np.abs(d) * 1.01 + (K + 20) * U * 50)
+        _close("dx", _host(self.dx), d * fac[1], HALF["bf16"] * np.abs(d * fac[1]) * 1.01 + (K + 20) * U * 70)
+        dx = _host(self.dx)
+        want = {"w": [], "b": [], "table": [], "other": []}
+        size = {k: [] for k in want}
+        for g in range(R):
+            at = slice(g * n, (g + 1) * n)
+            _, dw, db, aw, ab = T.norm_grad(_host(self.dy)[at], hv[at], mean[at], rstd[at], self.params["w"], None, False)
+            dt, st = T.embedding_grad(tok[at], dx[at], V, 4.0, fac[0][at])
+            other = np.full((5, 3), float(g))
+            for k, v, a in (("w", dw, aw), ("b", db, ab), ("table", dt, st), ("other", other, other)):
+                want[k].append(v)
+                size[k].append(a)
+        # rank s of each shard group holds chunk s of the average over all ranks
+        for k, (i, j) in self.at.items():
+            fb = self.buckets[i]
+            avg, mag = np.mean(want[k], 0), np.mean(size[k], 0)
+            lay = fb.layout
+            for g in range(R):
+                a, rows = lay.row_off[j][g % S], lay.row_len[j][g % S]
+                got = _host(fb.rs_out[g][lay.in_off[j]:lay.in_off[j] + avg[a:a + rows].size])
+                # n + 8 roundings of a rank's sum, then one per operand and two divisions
+                _close(f"{k} on rank {g}", got, avg[a:a + rows].reshape(-1),
+                       (n + 8 + R + 2) * U * mag[a:a + rows].reshape(-1) + TINY["f32"])
+
+
+@pytest.mark.parametrize("one_bucket", [False, True])
+@pytest.mark.parametrize("fused_rs", [False, True])
+def test_layer_through_the_path(one_bucket, fused_rs):
+    require_gpu()
+    note(f"[path] one_bucket={one_bucket} fused_rs={fused_rs}")
+    layer = _Layer(1, one_bucket)
+    layer.forward()
+    layer.norm_backward()
+    layer.table_backward()
+    for fb in layer.buckets:
+        for step in (["rs_copy_reduce"] if fused_rs else ["rs_copy_in", "rs_reduce"]) + ["fused_ar"]:
+            fb.run(step)
+    torch.cuda.synchronize()
+    layer.check()
+
+
+@pytest.mark.parametrize("how", ["pipelined", "serial", "graph"])
+def test_layer_through_the_backward_pipeline(how):
+    """The pipeline issues each bucket's gradients and starts its RS behind
+    them; captured, it replays with new inputs."""
+    require_gpu()
+    note(f"[path] pipeline {how}")
+    layer = _Layer(2)
+    layer.forward()
+    pipe = hp.BackwardPipeline(layer.buckets, backward=[layer.norm_backward, layer.table_backward])
+    if how == "graph":
+        graph = pipe.graph()
+        for k in range(3):
+            layer.dy.mul_(-0.5)  # exact
+            layer.dx.fill_(float("nan"))
+            for fb in layer.buckets:
+                for t in fb.fused:
+                    t.fill_(float("nan"))
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            layer.check()
+    else:
+        (pipe.run_pipelined if how == "pipelined" else pipe.run_serial)()
+        torch.cuda.synchronize()
+        layer.check()
+
+
+def test_bucket_refusals():
+    require_gpu()
+    fb = hp.FlatBucket([(6, 4), (4,)], 2, 2, torch.float32, device="cuda")
+    x = torch.zeros(2, 4, device="cuda")
+    with pytest.raises(RuntimeError, match="bind"):
+        fb.norm_grad(1, x, x, torch.ones(2, device="cuda"), torch.empty_like(x), kind=hp.RMS)
+    with pytest.raises(ValueError, match="callables"):
+        hp.BackwardPipeline([fb], backward=[])
