@@ -87,7 +87,7 @@ struct NormGradArgs {
   void* dx;  // nullptr: not written
   void* const* dweight;
   void* const* dbias;  // nullptr: none
-  float* part;         // [n_ranks][blocks][1 or 2][cols]
+  float* part;          // [n_ranks][blocks][1 or 2][cols]
   uint64_t rows, cols;  // rows of one rank
   float factor;
   int n_ranks, blocks, rms, dtype, weight_dtype, grad_dtype, accumulate;
@@ -98,6 +98,9 @@ struct NormGradArgs {
 // partial sums per rank): a function of the sizes only, so that the order of
 // every sum is fixed.
 int norm_grad_blocks(uint64_t rows, uint64_t cols, int n_ranks);
+
+// Whether a norm gradient is one launch (and needs no workspace).
+bool norm_grad_few(uint64_t rows, uint64_t cols, int n_ranks);
 
 // Sorted positions per piece: as many as still give every SIMD of the chip
 // several waves.

@@ -229,6 +229,20 @@ __device__ __forceinline__ void store_any(int dtype, void* base, uint64_t at, ui
     store_cols<FSDP_F16, N>(base, at, n, v);
 }
 
+// One element.
+__device__ __forceinline__ float load_one(int dtype, const void* base, uint64_t i) {
+  if (dtype == FSDP_F32) return gmem<float>(base)[i];
+  const uint16_t x = gmem<uint16_t>(base)[i];
+  return dtype == FSDP_BF16 ? Elem<FSDP_BF16>::get(x) : Elem<FSDP_F16>::get(x);
+}
+
+__device__ __forceinline__ void store_one(int dtype, void* base, uint64_t i, float x) {
+  if (dtype == FSDP_F32)
+    gmem<float>(base)[i] = x;
+  else
+    gmem<uint16_t>(base)[i] = dtype == FSDP_BF16 ? Elem<FSDP_BF16>::put(x) : Elem<FSDP_F16>::put(x);
+}
+
 __device__ __forceinline__ int64_t token_at(const void* tokens, uint64_t i, int bytes) {
   return bytes == 8 ? gmem<int64_t>(tokens)[i] : (int64_t)gmem<int32_t>(tokens)[i];
 }
@@ -1068,6 +1082,78 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(fsdp::NormArgs a, uint3
 
 // --- norm gradient ----------------------------------------------------------------
 
+// A column sum into (or added to) element c of a gradient.
+__device__ __forceinline__ void put_sum(const fsdp::NormGradArgs& a, void* out, uint64_t c, float t) {
+  store_one(a.grad_dtype, out, c, a.accumulate ? load_one(a.grad_dtype, out, c) + t : t);
+}
+
+// What a call of few rows has beside NormGradArgs.
+template <bool FEW>
+struct FewArgs {};
+template <>
+struct FewArgs<true> {
+  uint32_t row_blocks;
+  fsdp::RankPtrs dweight, dbias;
+};
+
+// dweight and dbias of 512 columns of one rank: a wave takes every WAVESth
+// row, 8 columns a lane, kFewAhead rows in flight; then the waves' sums in a
+// fixed order.
+constexpr int kFewAhead = 4;
+
+template <int D, int WAVES>
+__device__ __forceinline__ void sum_columns(const fsdp::NormGradArgs& a, const FewArgs<true>& few, uint32_t block) {
+  __shared__ float sums[2][WAVES][64 * kGroup];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint64_t g = blockIdx.y;
+  const uint32_t j = block * 64 + lane, len = group_len(a.cols, j);
+  float dw[8] = {}, db[8] = {};
+  if (len) {
+    for (uint64_t r = wave; r < a.rows; r += WAVES * kFewAhead) {
+      Raw<D> h[kFewAhead], dy[kFewAhead];
+      float mean[kFewAhead], rstd[kFewAhead];
+#pragma unroll
+      for (int u = 0; u < kFewAhead; ++u) {
+        h[u] = dy[u] = Raw<D>{};
+        mean[u] = rstd[u] = 0.0f;
+        if (r + u * WAVES < a.rows) {
+          const uint64_t row = g * a.rows + r + u * WAVES, at = row * a.cols + (uint64_t)j * kGroup;
+          h[u] = load_raw<D>(a.h, at, len);
+          dy[u] = load_raw<D>(a.dy, at, len);
+          if (a.mean) mean[u] = gmem<float>(a.mean)[row];
+          rstd[u] = gmem<float>(a.rstd)[row];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kFewAhead; ++u) {
+        float x[8], d[8];
+        unpack<D>(h[u], x);
+        unpack<D>(dy[u], d);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          dw[k] = __builtin_fmaf(d[k], (x[k] - mean[u]) * rstd[u], dw[k]);
+          db[k] += d[k];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    sums[0][wave][lane + 64 * k] = dw[k];
+    sums[1][wave][lane + 64 * k] = db[k];
+  }
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < 2 * 64 * kGroup; i += WAVES * 64) {
+    const uint32_t s = i / (64 * kGroup), e = i % (64 * kGroup);
+    const uint64_t c = ((uint64_t)block * 64 + e % 64) * kGroup + e / 64;
+    if (c >= a.cols || (s && !a.dbias)) continue;
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) t += sums[s][w][e];
+    put_sum(a, s ? few.dbias.p[blockIdx.y] : few.dweight.p[blockIdx.y], c, t);
+  }
+}
+
 // With xhat = (h - mean) * rstd and g = dy * weight, row by row:
 //   dres = rstd * (g - mean(g) - xhat * mean(g * xhat)) + dh
 //   dx   = drop'(dres)
@@ -1077,15 +1163,27 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(fsdp::NormArgs a, uint3
 // of `part`, after its waves' sums were added in LDS in a fixed order.  The
 // next row's loads are in flight while a row is computed.  Absent columns
 // load as dy = 0 and add nothing.
-template <int D, int LANES, int NV, bool DROP>
-__global__ __launch_bounds__(block_of(LANES)) void norm_grad_kernel(fsdp::NormGradArgs a) {
+//
+// FEW: a call of few rows in one launch.  The column sums need no row sum, so
+// workgroups of their own (the ones from row_blocks on) read dy and h once
+// more and write dweight and dbias; the others leave the column sums out.
+template <int D, int LANES, int NV, bool DROP, bool FEW>
+__global__ __launch_bounds__(block_of(LANES)) void norm_grad_kernel(fsdp::NormGradArgs a, FewArgs<FEW> few) {
+  if constexpr (FEW) {
+    if (blockIdx.x >= few.row_blocks) {
+      sum_columns<D, block_of(LANES) / 64>(a, few, blockIdx.x - few.row_blocks);
+      return;
+    }
+  }
   constexpr int kBlockSize = block_of(LANES);
   constexpr int kRows = kBlockSize / LANES;
   constexpr uint32_t kWidth = LANES * NV * kGroup;  // columns the lanes of a row cover
   __shared__ float lds[2][2][LANES < 64 ? 1 : LANES / 64];
-  __shared__ float cross[kRows > 1 ? kRows * kWidth : 1];
+  __shared__ float cross[kRows > 1 && !FEW ? kRows * kWidth : 1];
   const uint32_t l = threadIdx.x % LANES, sub = threadIdx.x / LANES;
-  const uint64_t g = blockIdx.y, step = (uint64_t)gridDim.x * kRows;
+  uint64_t blocks = gridDim.x;
+  if constexpr (FEW) blocks = few.row_blocks;
+  const uint64_t g = blockIdx.y, step = blocks * kRows;
   uint64_t r = (uint64_t)blockIdx.x * kRows + sub;
   uint32_t len[NV];
   Raw<D> h[NV], dy[NV], dh[NV];
@@ -1127,8 +1225,10 @@ __global__ __launch_bounds__(block_of(LANES)) void norm_grad_kernel(fsdp::NormGr
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         x[i][k] = (x[i][k] - mean) * rstd;
-        dw[i][k] = __builtin_fmaf(gw[i][k], x[i][k], dw[i][k]);
-        db[i][k] += gw[i][k];
+        if constexpr (!FEW) {
+          dw[i][k] = __builtin_fmaf(gw[i][k], x[i][k], dw[i][k]);
+          db[i][k] += gw[i][k];
+        }
         gw[i][k] *= w[i][k];
         s0 += gw[i][k];
         s1 = __builtin_fmaf(gw[i][k], x[i][k], s1);
@@ -1165,6 +1265,7 @@ __global__ __launch_bounds__(block_of(LANES)) void norm_grad_kernel(fsdp::NormGr
       }
     }
   }
+  if constexpr (FEW) return;
   const uint32_t sums = a.dbias ? 2 : 1;
   float* part = a.part + ((g * gridDim.x + blockIdx.x) * sums) * a.cols;
   for (uint32_t s = 0; s < sums; ++s) {
@@ -1291,18 +1392,7 @@ __global__ __launch_bounds__(kJoinWaves * 64) void norm_join_kernel(fsdp::NormGr
     t = 0.0f;
 #pragma unroll
     for (int w = 0; w < kJoinWaves; ++w) t += lds[w][lane];
-    void* out = s ? dbias.p[blockIdx.y] : dweight.p[blockIdx.y];
-    float v[1] = {t};
-    if (a.grad_dtype == FSDP_F32) {
-      GMEM float* p = gmem<float>(out) + c;
-      *p = a.accumulate ? *p + v[0] : v[0];
-    } else {
-      GMEM uint16_t* p = gmem<uint16_t>(out) + c;
-      if (a.grad_dtype == FSDP_BF16)
-        *p = Elem<FSDP_BF16>::put(a.accumulate ? Elem<FSDP_BF16>::get(*p) + v[0] : v[0]);
-      else
-        *p = Elem<FSDP_F16>::put(a.accumulate ? Elem<FSDP_F16>::get(*p) + v[0] : v[0]);
-    }
+    put_sum(a, s ? dbias.p[blockIdx.y] : dweight.p[blockIdx.y], c, t);
   }
 }
 
@@ -1327,6 +1417,14 @@ uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
 Launch launch_of(void* stream, void* start, void* stop) {
   return Launch{static_cast<hipStream_t>(stream), static_cast<hipEvent_t>(start), static_cast<hipEvent_t>(stop)};
+}
+
+// The pointers of ranks [first, first + n), or none.
+fsdp::RankPtrs rank_ptrs(void* const* p, int first, int n) {
+  fsdp::RankPtrs r = {};
+  if (p)
+    for (int k = 0; k < n; ++k) r.p[k] = p[first + k];
+  return r;
 }
 
 template <int TD, int OD>
@@ -1382,11 +1480,22 @@ int norm_go(const Launch& go, const fsdp::NormArgs& a) {
   return go(norm_wide_kernel<D, false>, grid, 1024, true, true, a, groups);
 }
 
+bool few_rows(const fsdp::NormGradArgs& a) { return fsdp::norm_grad_few(a.rows, a.cols, a.n_ranks); }
+
 template <int D, int LANES, int NV>
 int norm_grad_rows(const Launch& go, const fsdp::NormGradArgs& a) {
+  constexpr int block = block_of(LANES);
+  const bool drop = a.drop.state;
+  if (few_rows(a)) {
+    const FewArgs<true> few{(uint32_t)ceil_div(a.rows, block / LANES), rank_ptrs(a.dweight, 0, a.n_ranks),
+                            rank_ptrs(a.dbias, 0, a.n_ranks)};
+    const dim3 grid(few.row_blocks + (uint32_t)ceil_div(a.cols, 64 * kGroup), (uint32_t)a.n_ranks);
+    if (drop) return go(norm_grad_kernel<D, LANES, NV, true, true>, grid, block, true, true, a, few);
+    return go(norm_grad_kernel<D, LANES, NV, false, true>, grid, block, true, true, a, few);
+  }
   const dim3 grid((uint32_t)a.blocks, (uint32_t)a.n_ranks);
-  if (a.drop.state) return go(norm_grad_kernel<D, LANES, NV, true>, grid, block_of(LANES), true, false, a);
-  return go(norm_grad_kernel<D, LANES, NV, false>, grid, block_of(LANES), true, false, a);
+  if (drop) return go(norm_grad_kernel<D, LANES, NV, true, false>, grid, block, true, false, a, FewArgs<false>{});
+  return go(norm_grad_kernel<D, LANES, NV, false, false>, grid, block, true, false, a, FewArgs<false>{});
 }
 
 template <int D>
@@ -1449,8 +1558,7 @@ int embedding_grad_go(const Launch& go, const fsdp::EmbedGradArgs& a) {
   if (p.small) {
     for (int g0 = 0; g0 < a.n_ranks; g0 += fsdp::kMaxRankPtrs) {
       const int n = a.n_ranks - g0 < fsdp::kMaxRankPtrs ? a.n_ranks - g0 : fsdp::kMaxRankPtrs;
-      fsdp::RankPtrs ptrs = {};
-      for (int k = 0; k < n; ++k) ptrs.p[k] = a.grads[g0 + k];
+      const fsdp::RankPtrs ptrs = rank_ptrs(a.grads, g0, n);
       const int rc = go(embedding_grad_small_kernel<D, DROP, ADD>, dim3((uint32_t)p.small, (uint32_t)n), kSmallBlock, g0 == 0,
                         g0 + n == a.n_ranks, a, ptrs, (uint32_t)g0, grid);
       if (rc) return rc;
@@ -1464,8 +1572,7 @@ int embedding_grad_go(const Launch& go, const fsdp::EmbedGradArgs& a) {
   for (int g0 = 0; g0 < a.n_ranks; g0 += fsdp::kMaxRankPtrs) {
     const int n = a.n_ranks - g0 < fsdp::kMaxRankPtrs ? a.n_ranks - g0 : fsdp::kMaxRankPtrs;
     const bool end = g0 + n == a.n_ranks;
-    fsdp::RankPtrs ptrs = {};
-    for (int k = 0; k < n; ++k) ptrs.p[k] = a.grads[g0 + k];
+    const fsdp::RankPtrs ptrs = rank_ptrs(a.grads, g0, n);
     if (!ADD)
       rc = go(embedding_fill_kernel, dim3((uint32_t)p.fill, (uint32_t)n), kFillBlock, false, end && !p.pieces, a, ptrs,
               (uint32_t)g0, grid);
@@ -1487,6 +1594,14 @@ int embedding_grad_drop(const Launch& go, const fsdp::EmbedGradArgs& a) {
 }
 
 }  // namespace
+
+// One launch for up to 128 rows a rank, while a column workgroup's 16 waves
+// have few rows each.  Measured on MI355X with the call's host side, us (us
+// in two launches): 1 rank, 128 x 1024 13 (17), 256 x 1024 20 (17); 8 ranks,
+// 128 x 4096 17 (21), 256 x 4096 26 (23).
+bool fsdp::norm_grad_few(uint64_t rows, uint64_t cols, int n_ranks) {
+  return rows && rows <= 128 && n_ranks <= kMaxRankPtrs && cols <= 8192;
+}
 
 // Workgroups over all ranks, and at least one row for each of a workgroup's
 // rows in flight.  Measured on MI355X, us (us with the other count): 256
@@ -1553,15 +1668,11 @@ int fsdp_launch_norm_grad(const fsdp::NormGradArgs& a, void* stream, void* start
     case FSDP_BF16: rc = norm_grad_go<FSDP_BF16>(go, a); break;
     default: rc = norm_grad_go<FSDP_F16>(go, a); break;
   }
+  if (few_rows(a)) return rc;  // the first launch was all
   for (int g0 = 0; !rc && g0 < a.n_ranks; g0 += fsdp::kMaxRankPtrs) {
     const int n = a.n_ranks - g0 < fsdp::kMaxRankPtrs ? a.n_ranks - g0 : fsdp::kMaxRankPtrs;
-    fsdp::RankPtrs w = {}, b = {};
-    for (int k = 0; k < n; ++k) {
-      w.p[k] = a.dweight[g0 + k];
-      if (a.dbias) b.p[k] = a.dbias[g0 + k];
-    }
     rc = go(norm_join_kernel, dim3((uint32_t)ceil_div(a.cols, 64), (uint32_t)n, a.dbias ? 2 : 1), kJoinWaves * 64, false,
-            g0 + n == a.n_ranks, a, w, b, (uint32_t)g0);
+            g0 + n == a.n_ranks, a, rank_ptrs(a.dweight, g0, n), rank_ptrs(a.dbias, g0, n), (uint32_t)g0);
   }
   return rc;
 }

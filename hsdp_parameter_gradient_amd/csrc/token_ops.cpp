@@ -25,6 +25,11 @@ struct Buffers {
   std::vector<Span> outs, ins;
   int rc = FSDP_OK;
 
+  Buffers() {
+    outs.reserve(16);
+    ins.reserve(16);
+  }
+
   void add(std::vector<Span>& to, const void* p, int64_t count, int64_t bytes, uint64_t align, const char* what,
            long idx) {
     if (rc) return;
@@ -158,6 +163,7 @@ int embedding_grad_workspace_impl(int32_t n_ranks, int64_t n_tokens, int64_t voc
 }
 
 int check_workspace(const void* p, int64_t have, int64_t need) {
+  if (need == 0) return FSDP_OK;
   if (have < need) return fail(FSDP_EINVAL, "workspace of %lld bytes, %lld needed", (long long)have, (long long)need);
   if (!p) return fail(FSDP_EINVAL, "workspace is NULL");
   if ((uint64_t)p % 16) return fail(FSDP_EALIGN, "workspace = %p is not 16-byte aligned", p);
@@ -263,6 +269,10 @@ int norm_workspace(int32_t n_ranks, int64_t rows, int64_t cols, int* blocks, int
   if ((rc = check_ranks(n_ranks)) || (rc = check_count(rows, 0, "rows")) || (rc = check_count(cols, 1, "cols")))
     return rc;
   *blocks = fsdp::norm_grad_blocks(rows, cols, n_ranks);
+  if (fsdp::norm_grad_few(rows, cols, n_ranks)) {
+    *bytes = 0;
+    return FSDP_OK;
+  }
   if (!mul_ok((int64_t)*blocks * n_ranks * 8, cols, bytes)) return fail(FSDP_EINVAL, "workspace size overflow");
   return FSDP_OK;
 }

@@ -138,7 +138,7 @@ class _Prepared(B._Call):
 
     def __init__(self, name: str, args: tuple, keep: tuple, at: Optional[int] = None, nbytes: int = 0):
         super().__init__(name, args, keep)
-        if at is not None:
+        if nbytes:
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError(f"{name}: prepare the call before the capture (its workspace outlives the graph)")
             self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=_torch_device(self.device))
@@ -287,8 +287,10 @@ def fsdp_norm_grad(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight
     dx that of x (drop'(dres)); dweight[g] and dbias[g] those of rank g's
     rows, R = len(dweight) ranks one after the other."""
     args, dev = _norm_grad(dy, h, rstd, weight, dres, dweight, mean, dbias, dh, dx, kind, dropout, accumulate)
-    ws = _workspace(args[-1], dev, stream)
-    _issue("fsdp_norm_grad", args[:_NORM_AT] + (ws.data_ptr(), args[-1]), dev, stream)
+    if args[-1]:
+        ws = _workspace(args[-1], dev, stream)
+        args = args[:_NORM_AT] + (ws.data_ptr(), args[-1])
+    _issue("fsdp_norm_grad", args, dev, stream)
 
 
 # --- prepared calls (prepare): the signatures of the calls, without the stream ---

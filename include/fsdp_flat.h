@@ -381,7 +381,8 @@ int fsdp_norm(int32_t kind, int64_t rows, int64_t cols, int32_t dtype, int32_t w
  *   dh, dx, dbias  may be NULL (dx not with a dropout)
  *   mean           read for FSDP_LAYER_NORM only
  *   dweight, dbias [n_ranks] device pointers (host arrays), cols of grad_dtype
- *   workspace      fsdp_norm_grad_workspace bytes, 16-byte aligned
+ *   workspace      fsdp_norm_grad_workspace bytes, 16-byte aligned (NULL
+ *                  where that is 0)
  */
 int fsdp_norm_grad_workspace(int32_t n_ranks, int64_t rows, int64_t cols, int64_t* bytes);
 int fsdp_norm_grad(int32_t kind, int32_t n_ranks, int64_t rows, int64_t cols, int32_t dtype, int32_t weight_dtype,

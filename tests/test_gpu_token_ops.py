@@ -249,6 +249,10 @@ NORM = [  # rows, cols, act, weight, kind, bias, residual, p, mean of x
     (2, 16392, "bf16", "bf16", "layer", True, True, 0.1, 0.0),
     (3, 20001, "f32", "f32", "rms", False, False, 0.0, 0.0),
     (3, 40007, "f16", "f32", "layer", True, True, 0.0, 0.0),
+    # more rows than workgroups
+    (33000, 16, "bf16", "bf16", "layer", True, True, 0.0, 0.0),
+    (9001, 65, "f32", "f32", "rms", False, True, 0.0, 0.0),
+    (9000, 514, "bf16", "f32", "layer", True, False, 0.0, 0.0),
 ]
 
 
@@ -309,6 +313,18 @@ NGRAD = [  # ranks, rows, cols, act, weight, grad, kind, bias, dh, p, accumulate
     (2, 2, 8193, "bf16", "bf16", "f32", "layer", True, True, 0.1, False),
     (1, 3, 16385, "f32", "f32", "f32", "layer", True, True, 0.0, True),
     (1, 3, 30011, "f16", "f32", "bf16", "rms", False, False, 0.0, False),
+    # beyond the rows of the one-launch kernel, every way of laying a row over lanes
+    (2, 129, 24, "bf16", "bf16", "f32", "layer", True, True, 0.1, False),
+    (1, 200, 330, "f16", "f32", "f16", "layer", True, False, 0.0, True),
+    (2, 131, 1000, "bf16", "f32", "f32", "layer", True, True, 0.0, False),
+    (1, 300, 2047, "f32", "f32", "f32", "rms", False, True, 0.2, False),
+    (2, 129, 4096, "bf16", "bf16", "bf16", "layer", True, True, 0.0, True),
+    (1, 140, 5003, "bf16", "bf16", "f32", "layer", True, True, 0.1, False),
+    (1, 290, 8192, "f16", "f16", "f32", "rms", False, False, 0.0, False),
+    (70, 130, 9, "f32", "f32", "f32", "layer", True, True, 0.0, False),
+    (64, 3, 70, "f32", "f32", "f32", "layer", True, True, 0.0, True),
+    (65, 3, 70, "f32", "f32", "f32", "layer", True, True, 0.0, False),
+    (1, 128, 1025, "bf16", "bf16", "f32", "layer", True, False, 0.0, False),
 ]
 
 

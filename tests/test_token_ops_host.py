@@ -156,8 +156,8 @@ REFUSED = [
     ("fsdp_norm_grad", dict(dx=None, dropout=_drop()), 1), ("fsdp_norm_grad", dict(dweight=None), 1),
     ("fsdp_norm_grad", dict(dbias=_ptrs([BASE + (8 << 32), BASE + (9 << 32)])), 5),
     ("fsdp_norm_grad", dict(dres=BASE), 5), ("fsdp_norm_grad", dict(dres=BASE + (1 << 32)), 5),
-    ("fsdp_norm_grad", dict(dx=BASE + (6 << 32)), 5), ("fsdp_norm_grad", dict(workspace_bytes=16), 1),
-    ("fsdp_norm_grad", dict(workspace=None), 1), ("fsdp_norm_grad", dict(dweight=_ptrs([0, BASE + (8 << 32)])), 1),
+    ("fsdp_norm_grad", dict(dx=BASE + (6 << 32)), 5), ("fsdp_norm_grad", dict(rows=200, workspace_bytes=16), 1),
+    ("fsdp_norm_grad", dict(rows=200, workspace=None), 1), ("fsdp_norm_grad", dict(dweight=_ptrs([0, BASE + (8 << 32)])), 1),
     ("fsdp_norm_grad", dict(rows=1 << 30, n_ranks=8, dropout=_drop()), 1),
 ]
 
@@ -186,6 +186,8 @@ def test_workspace_queries():
     assert hp.fsdp_embedding_grad_workspace(1, 32, 100, 8) == 512 + 512
     assert hp.fsdp_embedding_grad_workspace(2, 65, 100, 8) == 1024 + 2304 + 2 * 17 * 2 * 8 * 4
     assert hp.fsdp_norm_grad_workspace(1, 0, 8) == 2 * 8 * 4
+    assert hp.fsdp_norm_grad_workspace(8, 128, 8192) == 0  # one launch, no partial sums
+    assert hp.fsdp_norm_grad_workspace(8, 129, 8192) > 0 and hp.fsdp_norm_grad_workspace(8, 1, 8193) > 0
     assert hp.fsdp_norm_grad_workspace(8, 1 << 20, 4096) % (8 * 2 * 4096 * 4) == 0
     for call in (lambda: hp.fsdp_embedding_grad_workspace(0, 1, 1, 1), lambda: hp.fsdp_norm_grad_workspace(1, 1, 0),
                  lambda: hp.fsdp_embedding_grad_workspace(1, -1, 1, 1), lambda: hp.fsdp_norm_grad_workspace(1, 1 << 31, 8),
