@@ -1096,28 +1096,30 @@ struct FewArgs<true> {
   fsdp::RankPtrs dweight, dbias;
 };
 
-// dweight and dbias of 512 columns of one rank: a wave takes every WAVESth
-// row, 8 columns a lane, kFewAhead rows in flight; then the waves' sums in a
-// fixed order.
+// dweight and dbias of kFewCols columns of one rank: 16 lanes side by side, 8
+// columns each, so a workgroup takes 4 * WAVES rows at a time, kFewAhead times
+// that in flight; then its row groups' sums in a fixed order.
 constexpr int kFewAhead = 4;
+constexpr uint32_t kFewCols = 16 * kGroup;
 
 template <int D, int WAVES>
 __device__ __forceinline__ void sum_columns(const fsdp::NormGradArgs& a, const FewArgs<true>& few, uint32_t block) {
-  __shared__ float sums[2][WAVES][64 * kGroup];
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr uint32_t kParts = 4 * WAVES;
+  __shared__ float sums[2][kParts][kFewCols];
+  const uint32_t lane = threadIdx.x & 15, part = threadIdx.x >> 4;
   const uint64_t g = blockIdx.y;
-  const uint32_t j = block * 64 + lane, len = group_len(a.cols, j);
+  const uint32_t j = block * 16 + lane, len = group_len(a.cols, j);
   float dw[8] = {}, db[8] = {};
   if (len) {
-    for (uint64_t r = wave; r < a.rows; r += WAVES * kFewAhead) {
+    for (uint64_t r = part; r < a.rows; r += kParts * kFewAhead) {
       Raw<D> h[kFewAhead], dy[kFewAhead];
       float mean[kFewAhead], rstd[kFewAhead];
 #pragma unroll
       for (int u = 0; u < kFewAhead; ++u) {
         h[u] = dy[u] = Raw<D>{};
         mean[u] = rstd[u] = 0.0f;
-        if (r + u * WAVES < a.rows) {
-          const uint64_t row = g * a.rows + r + u * WAVES, at = row * a.cols + (uint64_t)j * kGroup;
+        if (r + u * kParts < a.rows) {
+          const uint64_t row = g * a.rows + r + u * kParts, at = row * a.cols + (uint64_t)j * kGroup;
           h[u] = load_raw<D>(a.h, at, len);
           dy[u] = load_raw<D>(a.dy, at, len);
           if (a.mean) mean[u] = gmem<float>(a.mean)[row];
@@ -1139,17 +1141,17 @@ __device__ __forceinline__ void sum_columns(const fsdp::NormGradArgs& a, const F
   }
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    sums[0][wave][lane + 64 * k] = dw[k];
-    sums[1][wave][lane + 64 * k] = db[k];
+    sums[0][part][lane + 16 * k] = dw[k];
+    sums[1][part][lane + 16 * k] = db[k];
   }
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < 2 * 64 * kGroup; i += WAVES * 64) {
-    const uint32_t s = i / (64 * kGroup), e = i % (64 * kGroup);
-    const uint64_t c = ((uint64_t)block * 64 + e % 64) * kGroup + e / 64;
+  for (uint32_t i = threadIdx.x; i < 2 * kFewCols; i += WAVES * 64) {
+    const uint32_t s = i / kFewCols, e = i % kFewCols;
+    const uint64_t c = ((uint64_t)block * 16 + e % 16) * kGroup + e / 16;
     if (c >= a.cols || (s && !a.dbias)) continue;
     float t = 0.0f;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) t += sums[s][w][e];
+    for (uint32_t q = 0; q < kParts; ++q) t += sums[s][q][e];
     put_sum(a, s ? few.dbias.p[blockIdx.y] : few.dweight.p[blockIdx.y], c, t);
   }
 }
@@ -1489,7 +1491,7 @@ int norm_grad_rows(const Launch& go, const fsdp::NormGradArgs& a) {
   if (few_rows(a)) {
     const FewArgs<true> few{(uint32_t)ceil_div(a.rows, block / LANES), rank_ptrs(a.dweight, 0, a.n_ranks),
                             rank_ptrs(a.dbias, 0, a.n_ranks)};
-    const dim3 grid(few.row_blocks + (uint32_t)ceil_div(a.cols, 64 * kGroup), (uint32_t)a.n_ranks);
+    const dim3 grid(few.row_blocks + (uint32_t)ceil_div(a.cols, kFewCols), (uint32_t)a.n_ranks);
     if (drop) return go(norm_grad_kernel<D, LANES, NV, true, true>, grid, block, true, true, a, few);
     return go(norm_grad_kernel<D, LANES, NV, false, true>, grid, block, true, true, a, few);
   }
@@ -1595,12 +1597,16 @@ int embedding_grad_drop(const Launch& go, const fsdp::EmbedGradArgs& a) {
 
 }  // namespace
 
-// One launch for up to 128 rows a rank, while a column workgroup's 16 waves
-// have few rows each.  Measured on MI355X with the call's host side, us (us
-// in two launches): 1 rank, 128 x 1024 13 (17), 256 x 1024 20 (17); 8 ranks,
-// 128 x 4096 17 (21), 256 x 4096 26 (23).
+// One launch for up to 512 rows a rank and 2^23 elements: a column workgroup
+// then has few rounds over the rows, and dy and h come from L2 the second
+// time.  Measured on MI355X with the call's host side, us (us in two
+// launches): 1 rank, 512 x 1024 10.7 (15.5), 1024 x 1024 20 (14); 8 ranks,
+// 256 x 4096 20 (22), 512 x 4096 37 (34).
+constexpr uint64_t kFewRows = 512, kFewElements = uint64_t(1) << 23;
+
 bool fsdp::norm_grad_few(uint64_t rows, uint64_t cols, int n_ranks) {
-  return rows && rows <= 128 && n_ranks <= kMaxRankPtrs && cols <= 8192;
+  return rows && rows <= kFewRows && rows * (uint64_t)n_ranks * cols <= kFewElements && n_ranks <= kMaxRankPtrs &&
+         cols <= 8192;
 }
 
 // Workgroups over all ranks, and at least one row for each of a workgroup's

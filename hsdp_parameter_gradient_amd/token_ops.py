@@ -101,11 +101,16 @@ def _grads(grads: Sequence[torch.Tensor], what: str, n_ranks: int, numel: int, d
     return (ctypes.c_void_p * n_ranks)(*[_ptr(t, what, numel, dtype, device) for t in grads])
 
 
+_FN: dict = {}
+
+
 def _issue(name: str, args: tuple, device: int, stream) -> None:
     """The call on a stream of `device` (default: its current one)."""
-    st = B._stream(stream, device)
-    fn = getattr(B.lib(), name)
-    if torch.cuda.current_device() == device:
+    fn = _FN.get(name)
+    if fn is None:
+        fn = _FN[name] = getattr(B.lib(), name)
+    st = B._raw_stream(device) or None if stream is None and B._raw_stream is not None else B._stream(stream, device)
+    if (B._get_device() if B._get_device is not None else torch.cuda.current_device()) == device:
         rc = fn(*args, st)
     else:
         with torch.cuda.device(device):

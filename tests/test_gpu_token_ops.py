@@ -314,17 +314,18 @@ NGRAD = [  # ranks, rows, cols, act, weight, grad, kind, bias, dh, p, accumulate
     (1, 3, 16385, "f32", "f32", "f32", "layer", True, True, 0.0, True),
     (1, 3, 30011, "f16", "f32", "bf16", "rms", False, False, 0.0, False),
     # beyond the rows of the one-launch kernel, every way of laying a row over lanes
-    (2, 129, 24, "bf16", "bf16", "f32", "layer", True, True, 0.1, False),
-    (1, 200, 330, "f16", "f32", "f16", "layer", True, False, 0.0, True),
-    (2, 131, 1000, "bf16", "f32", "f32", "layer", True, True, 0.0, False),
-    (1, 300, 2047, "f32", "f32", "f32", "rms", False, True, 0.2, False),
-    (2, 129, 4096, "bf16", "bf16", "bf16", "layer", True, True, 0.0, True),
-    (1, 140, 5003, "bf16", "bf16", "f32", "layer", True, True, 0.1, False),
-    (1, 290, 8192, "f16", "f16", "f32", "rms", False, False, 0.0, False),
-    (70, 130, 9, "f32", "f32", "f32", "layer", True, True, 0.0, False),
+    (2, 513, 24, "bf16", "bf16", "f32", "layer", True, True, 0.1, False),
+    (1, 530, 330, "f16", "f32", "f16", "layer", True, False, 0.0, True),
+    (2, 531, 1000, "bf16", "f32", "f32", "layer", True, True, 0.0, False),
+    (1, 600, 2047, "f32", "f32", "f32", "rms", False, True, 0.2, False),
+    (2, 513, 4096, "bf16", "bf16", "bf16", "layer", True, True, 0.0, True),
+    (1, 513, 5003, "bf16", "bf16", "f32", "layer", True, True, 0.1, False),
+    (1, 520, 8192, "f16", "f16", "f32", "rms", False, False, 0.0, False),
+    (70, 13, 9, "f32", "f32", "f32", "layer", True, True, 0.0, False),
     (64, 3, 70, "f32", "f32", "f32", "layer", True, True, 0.0, True),
     (65, 3, 70, "f32", "f32", "f32", "layer", True, True, 0.0, False),
-    (1, 128, 1025, "bf16", "bf16", "f32", "layer", True, False, 0.0, False),
+    (1, 512, 1025, "bf16", "bf16", "f32", "layer", True, False, 0.0, False),
+    (3, 67, 4100, "bf16", "bf16", "f32", "layer", True, True, 0.1, False),
 ]
 
 
