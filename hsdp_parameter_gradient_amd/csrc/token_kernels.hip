@@ -889,6 +889,12 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float (*lds)[2][LAN
 constexpr uint32_t kNormRun = 64;
 constexpr int block_of(int lanes) { return lanes <= 64 ? 256 : lanes; }
 
+// 1 / sqrt(var + eps); a variance that rounding took below zero is zero (and a
+// NaN stays one).
+__device__ __forceinline__ float rstd_of(float var, float eps) {
+  return 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps);
+}
+
 // The columns of group j that exist: 8, fewer in a row's last group, 0 beyond.
 __device__ __forceinline__ uint32_t group_len(uint64_t cols, uint32_t j) {
   const uint64_t c = (uint64_t)j * kGroup;
@@ -987,7 +993,7 @@ __global__ __launch_bounds__(block_of(LANES)) void norm_kernel(fsdp::NormArgs a)
     row_sum2<LANES>(sum, sq, lds, slot);
     slot ^= 1;
     const float rest = a.rms ? 0.0f : sum * inv;
-    const float rstd = 1.0f / sqrtf((sq * inv - rest * rest) + a.eps);
+    const float rstd = rstd_of(sq * inv - rest * rest, a.eps);
     if (l == 0) {
       if (a.mean) a.mean[row] = mean + rest;
       if (a.rstd) a.rstd[row] = rstd;
@@ -1057,7 +1063,7 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(fsdp::NormArgs a, uint3
     }
     row_sum2<LANES>(sum, sq, lds, 1);
     const float rest = a.rms ? 0.0f : sum * inv;
-    const float rstd = 1.0f / sqrtf((sq * inv - rest * rest) + a.eps);
+    const float rstd = rstd_of(sq * inv - rest * rest, a.eps);
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mean + rest;
       if (a.rstd) a.rstd[row] = rstd;

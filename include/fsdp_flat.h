@@ -339,9 +339,8 @@ int fsdp_embedding(int64_t vocab, int64_t cols, int32_t table_dtype, int32_t out
 
 /*
  * grads[g][v] = scale * sum of drop'(dout[t]) over rank g's rows t with token
- * v, in ascending t for a token of up to 64 rows, else ascending within runs
- * of 64 whose sums are then added; drop' zeroes and scales as the lookup's
- * dropout did.  Tokens outside [0, vocab) add nothing.  With accumulate, rows
+ * v, in an order that the sizes and tokens fix; drop' zeroes and scales as the
+ * lookup's dropout did.  Tokens outside [0, vocab) add nothing.  With accumulate, rows
  * of grads without a token are neither read nor written.
  *   tokens     [n_ranks][n_tokens];  dout: [n_ranks * n_tokens] x cols of dtype
  *   grads      [n_ranks] device pointers (a host array), each vocab x cols of

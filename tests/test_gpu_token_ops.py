@@ -458,6 +458,19 @@ def test_constant_and_tiny_rows(cols):
     hp.fsdp_norm(x, w, y, bias=b, rstd=rstd)
     assert torch.equal(y[0], b) and torch.equal(y[2], b) and bool(torch.isfinite(y).all())
     _close("rstd", _host(rstd), np.full(3, float(np.float32(1e-5)) ** -0.5), 8 * U * 320)
+    # a variance that rounding takes below zero counts as zero: rstd is at most eps^-1/2
+    for c in (1e6 + 0.3, -77777.7, 3.0e5):
+        x.fill_(c)
+        hp.fsdp_norm(x, w, y, rstd=rstd, eps=1e-12)
+        assert bool(torch.isfinite(y).all()) and bool((rstd > 0).all()) and bool((rstd <= 1.00001e6).all()), c
+
+
+def test_lookup_in_an_empty_table():
+    require_gpu()
+    note("[values] empty table")
+    out = _out((5, 9), "bf16", 1)
+    hp.fsdp_embedding(torch.zeros(5, dtype=torch.int64, device="cuda"), torch.empty(0, 9, device="cuda"), out.view)
+    assert not bool(out.view.any()) and out.guards_intact()
 
 
 def test_seed_step_and_site_change_the_mask():
