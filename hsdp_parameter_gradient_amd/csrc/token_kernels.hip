@@ -406,6 +406,10 @@ __global__ __launch_bounds__(kEmbedBlock) void embedding_kernel(fsdp::EmbedArgs 
 // Then it places its lists: lanes of equal token find each other by one
 // ballot per bit of the token, whatever the mix.  A wave with more matches
 // than its list holds reads its tokens again.
+//
+// Bound by latency up to some 16 Ki tokens (MI355X: 8 x 2048 tokens of 32001
+// 9 us, 2 x 16383 of 4097 11 us), then by the workgroup that holds the
+// commonest tokens (65536 of 32001, frequencies 1 / rank: 62 us).
 constexpr int kSortBlock = 1024;
 constexpr int kSortWaves = kSortBlock / 64;
 constexpr uint32_t kSortMaxShift = 9;
@@ -568,7 +572,10 @@ __device__ __forceinline__ void zero_block(const fsdp::EmbedGradArgs& a, void* g
 }
 
 // The rows without a position, written as zeros (not when the gradient is
-// added to).
+// added to): bound by the HBM's write rate.  On MI355X 8 x 524 MB (4.06 GB of
+// it empty rows) in 607 us, 6.7 TB/s; in plain workgroup order 635, with 8
+// blocks a lane 655, 2 a lane 717, nontemporal stores 702, and in the launch
+// that sums the rows 790 for both (607 + 88 apart).
 __global__ __launch_bounds__(kFillBlock) void embedding_fill_kernel(fsdp::EmbedGradArgs a, fsdp::RankPtrs grads, uint32_t rank0,
                                           GradGrid grid) {
   const RankView rv = rank_view(a, rank0 + blockIdx.y);
@@ -599,6 +606,12 @@ constexpr int kCols = 4;  // columns of a lane where rows are summed: 16-byte fp
 // positions belongs to the piece that it begins in, whole; one with more is
 // summed piece by piece into `part` (slot 0: the piece's first token, slot 1:
 // another, which then reaches past its end).
+//
+// Bound by the chain from the order to the rows and on to the sums, so many
+// small waves: 2 rows ahead and 32 to 52 registers.  On MI355X 2 x 16383
+// tokens x 1021 fp16 with dropout 33 us (4 rows ahead 37, 8 columns a lane
+// 46); 8 x 2048 x 4096 bf16 88 us, 270 MB, with the fill's last stores still
+// draining (64 us behind nontemporal ones, which cost the fill more).
 template <int D, bool DROP, bool ADD>
 __global__ __launch_bounds__(kGradBlock) void embedding_grad_kernel(fsdp::EmbedGradArgs a, fsdp::RankPtrs grads,
                                                                     uint32_t rank0, GradGrid grid) {
@@ -683,7 +696,8 @@ __device__ __forceinline__ void put_grad(const fsdp::EmbedGradArgs& a, void* gra
 // A workgroup looks at the last tokens of the pieces of kJoinSpan sorted
 // positions and takes the ones that begin there, one after the other, 256
 // columns of them: its 16 waves add every sixteenth partial sum each, then the
-// waves' sums in a fixed order.
+// waves' sums in a fixed order.  Latency: 8 us for 2 x 16383 tokens, 16 us for
+// 65536 (54 with 4 waves and a workgroup per piece).
 constexpr int kJoinBlock = 1024;
 constexpr int kJoinSums = kJoinBlock / 64;
 constexpr uint32_t kJoinSpan = 128;
@@ -908,6 +922,11 @@ __device__ __forceinline__ uint32_t group_len(uint64_t cols, uint32_t j) {
 // and the next row's loads in flight.  The variance is the mean square of
 // h - mean, less the square of what rounding the mean left: a row far from
 // zero loses nothing.
+//
+// Bound by HBM: 16384 x 4096 bf16 with residual 537 MB in 97 us, 5.5 TB/s
+// (a plain copy: 6.4), the dropout hidden behind it; about 220 VALU
+// operations for 8 elements with it, half of what LDS shuffles, masks and
+// repeated conversions took before.
 template <int D, int LANES, int NV, bool DROP>
 __global__ __launch_bounds__(block_of(LANES)) void norm_kernel(fsdp::NormArgs a) {
   constexpr int kRows = block_of(LANES) / LANES;
@@ -1007,8 +1026,8 @@ __global__ __launch_bounds__(block_of(LANES)) void norm_kernel(fsdp::NormArgs a)
   }
 }
 
-// Rows too long for registers: h (or x) is read three times, the second and
-// third time mostly from L2.
+// Rows too long for registers (over 16384 columns): h (or x) is read three
+// times, the second and third time mostly from L2.  2048 x 20000 bf16 104 us.
 template <int D, bool DROP>
 __global__ __launch_bounds__(1024) void norm_wide_kernel(fsdp::NormArgs a, uint32_t groups) {
   constexpr int LANES = 1024;
@@ -1172,6 +1191,12 @@ __device__ __forceinline__ void sum_columns(const fsdp::NormGradArgs& a, const F
 // next row's loads are in flight while a row is computed.  Absent columns
 // load as dy = 0 and add nothing.
 //
+// Bound by HBM: 8 x 2048 x 4096 bf16 537 MB in 103 us, 5.2 TB/s; with dropout
+// 671 MB in 134 us.  LANES x NV is the fewest registers that hold a row: at
+// 4096 columns 512 x 1 (106 registers) 109 us a call, 256 x 2 (152) 120.
+// With dropout dres goes past the caches (143 -> 140 us): what is read next
+// is dx.
+//
 // FEW: a call of few rows in one launch.  The column sums need no row sum, so
 // workgroups of their own (the ones from row_blocks on) read dy and h once
 // more and write dweight and dbias; the others leave the column sums out.
@@ -1299,8 +1324,10 @@ __global__ __launch_bounds__(block_of(LANES)) void norm_grad_kernel(fsdp::NormGr
   }
 }
 
-// Rows too long for registers: two passes over the row, the column sums kept
-// in the workgroup's own rows of `part` (a lane reads back only what it wrote).
+// Rows too long for registers (over 8192 columns): two passes over the row, the
+// column sums kept in the workgroup's own rows of `part` (a lane reads back
+// only what it wrote), which L2 holds.  4096 x 16384 bf16 295 us: bound by the
+// sums' traffic; 4 groups a lane spilled registers.
 template <int D, bool DROP>
 __global__ __launch_bounds__(1024) void norm_grad_wide_kernel(fsdp::NormGradArgs a, uint32_t groups) {
   constexpr int LANES = 1024;
@@ -1380,7 +1407,8 @@ __global__ __launch_bounds__(1024) void norm_grad_wide_kernel(fsdp::NormGradArgs
 
 // A rank's dweight (and dbias): the column sums of its `blocks` partial rows.
 // A workgroup takes 64 columns of one of the two: 16 waves add every
-// sixteenth partial row, then the waves' sums in a fixed order.
+// sixteenth partial row, 8 in flight (4 us for 512 partial rows; 7 with one),
+// then the waves' sums in a fixed order.
 constexpr int kJoinWaves = 16;
 
 __global__ __launch_bounds__(kJoinWaves * 64) void norm_join_kernel(fsdp::NormGradArgs a, fsdp::RankPtrs dweight,
