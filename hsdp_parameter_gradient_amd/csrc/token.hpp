@@ -91,6 +91,7 @@ struct NormGradArgs {
   uint64_t rows, cols;  // rows of one rank
   float factor;
   int n_ranks, blocks, rms, dtype, weight_dtype, grad_dtype, accumulate;
+  int past_loads, past_stores;  // past the caches (set by the launcher)
   Drop drop;
 };
 

@@ -150,14 +150,23 @@ struct Raw {
   u32x4 w[D == FSDP_F32 ? 2 : 1];
 };
 
-template <int D>
+// PAST: loaded past the caches.  For 16-bit types only: the two halves of an
+// fp32 group come in two loads, and the second would fetch the line again.
+template <int D, bool PAST = false>
 __device__ __forceinline__ Raw<D> load_raw(const void* base, uint64_t at, uint32_t n) {
+  static_assert(!PAST || D != FSDP_F32, "one load per group");
   typedef typename Elem<D>::T T;
   const GMEM T* p = gmem<T>(base) + at;
   Raw<D> r;
   if (n >= 8) {
-    r.w[0] = *reinterpret_cast<const GMEM u32x4e*>(p);
-    if constexpr (D == FSDP_F32) r.w[1] = *reinterpret_cast<const GMEM u32x4e*>(p + 4);
+    if constexpr (D == FSDP_F32) {
+      r.w[0] = *reinterpret_cast<const GMEM u32x4e*>(p);
+      r.w[1] = *reinterpret_cast<const GMEM u32x4e*>(p + 4);
+    } else if constexpr (PAST) {
+      r.w[0] = __builtin_nontemporal_load(reinterpret_cast<const GMEM u32x4e*>(p));
+    } else {
+      r.w[0] = *reinterpret_cast<const GMEM u32x4e*>(p);
+    }
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -1200,7 +1209,7 @@ __device__ __forceinline__ void sum_columns(const fsdp::NormGradArgs& a, const F
 // FEW: a call of few rows in one launch.  The column sums need no row sum, so
 // workgroups of their own (the ones from row_blocks on) read dy and h once
 // more and write dweight and dbias; the others leave the column sums out.
-template <int D, int LANES, int NV, bool DROP, bool FEW>
+template <int D, int LANES, int NV, bool DROP, bool FEW, bool PAST>
 __global__ __launch_bounds__(block_of(LANES)) void norm_grad_kernel(fsdp::NormGradArgs a, FewArgs<FEW> few) {
   if constexpr (FEW) {
     if (blockIdx.x >= few.row_blocks) {
@@ -1226,9 +1235,9 @@ __global__ __launch_bounds__(block_of(LANES)) void norm_grad_kernel(fsdp::NormGr
     for (int i = 0; i < NV; ++i)
       if (len[i]) {
         const uint64_t at = row * a.cols + (uint64_t)(l + i * LANES) * kGroup;
-        h[i] = load_raw<D>(a.h, at, len[i]);
-        dy[i] = load_raw<D>(a.dy, at, len[i]);
-        if (a.dh) dh[i] = load_raw<D>(a.dh, at, len[i]);
+        h[i] = load_raw<D, PAST>(a.h, at, len[i]);
+        dy[i] = load_raw<D, PAST>(a.dy, at, len[i]);
+        if (a.dh) dh[i] = load_raw<D, PAST>(a.dh, at, len[i]);
       }
     if (a.mean) mean = gmem<float>(a.mean)[row];
     rstd = gmem<float>(a.rstd)[row];
@@ -1287,14 +1296,20 @@ __global__ __launch_bounds__(block_of(LANES)) void norm_grad_kernel(fsdp::NormGr
         const float d = __builtin_fmaf(-m1, x[i][k], gw[i][k] - m0);
         x[i][k] = __builtin_fmaf(rs, d, t[k]);
       }
-      store_cols<D, 8, DROP>(a.dres, p, len[i], x[i]);
+      if (DROP || a.past_stores)
+        store_cols<D, 8, true>(a.dres, p, len[i], x[i]);
+      else
+        store_cols<D, 8>(a.dres, p, len[i], x[i]);
       if (a.dx) {
         if constexpr (DROP) {
           drop_cols<8>(rng, (uint32_t)row, j, 0, x[i]);
 #pragma unroll
           for (int k = 0; k < 8; ++k) x[i][k] *= a.factor;
         }
-        store_cols<D, 8>(a.dx, p, len[i], x[i]);
+        if (a.past_stores)
+          store_cols<D, 8, true>(a.dx, p, len[i], x[i]);
+        else
+          store_cols<D, 8>(a.dx, p, len[i], x[i]);
       }
     }
   }
@@ -1526,12 +1541,19 @@ int norm_grad_rows(const Launch& go, const fsdp::NormGradArgs& a) {
     const FewArgs<true> few{(uint32_t)ceil_div(a.rows, block / LANES), rank_ptrs(a.dweight, 0, a.n_ranks),
                             rank_ptrs(a.dbias, 0, a.n_ranks)};
     const dim3 grid(few.row_blocks + (uint32_t)ceil_div(a.cols, kFewCols), (uint32_t)a.n_ranks);
-    if (drop) return go(norm_grad_kernel<D, LANES, NV, true, true>, grid, block, true, true, a, few);
-    return go(norm_grad_kernel<D, LANES, NV, false, true>, grid, block, true, true, a, few);
+    if (drop) return go(norm_grad_kernel<D, LANES, NV, true, true, false>, grid, block, true, true, a, few);
+    return go(norm_grad_kernel<D, LANES, NV, false, true, false>, grid, block, true, true, a, few);
   }
   const dim3 grid((uint32_t)a.blocks, (uint32_t)a.n_ranks);
-  if (drop) return go(norm_grad_kernel<D, LANES, NV, true, false>, grid, block, true, false, a, FewArgs<false>{});
-  return go(norm_grad_kernel<D, LANES, NV, false, false>, grid, block, true, false, a, FewArgs<false>{});
+  const FewArgs<false> none{};
+  if constexpr (D != FSDP_F32) {
+    if (a.past_loads) {
+      if (drop) return go(norm_grad_kernel<D, LANES, NV, true, false, true>, grid, block, true, false, a, none);
+      return go(norm_grad_kernel<D, LANES, NV, false, false, true>, grid, block, true, false, a, none);
+    }
+  }
+  if (drop) return go(norm_grad_kernel<D, LANES, NV, true, false, false>, grid, block, true, false, a, none);
+  return go(norm_grad_kernel<D, LANES, NV, false, false, false>, grid, block, true, false, a, none);
 }
 
 template <int D>
@@ -1700,8 +1722,16 @@ int fsdp_launch_norm(const fsdp::NormArgs& a, void* stream, void* start_event, v
   }
 }
 
-int fsdp_launch_norm_grad(const fsdp::NormGradArgs& a, void* stream, void* start_event, void* stop_event) {
+int fsdp_launch_norm_grad(const fsdp::NormGradArgs& args, void* stream, void* start_event, void* stop_event) {
   const Launch go = launch_of(stream, start_event, stop_event);
+  fsdp::NormGradArgs a = args;
+  // A call that moves more than the MALL holds reads its rows, each for the
+  // last time, past the caches, where lines are not shared between rows; one
+  // whose outputs alone fill the MALL also stores past them.
+  const uint64_t row = a.rows * (uint64_t)a.n_ranks * a.cols * (a.dtype == FSDP_F32 ? 4 : 2);
+  const uint64_t outs = row * (a.dx ? 2 : 1), ins = row * (a.dh ? 3 : 2);
+  a.past_loads = ins + outs >= kPastBytes && a.cols % kGroup == 0;
+  a.past_stores = outs >= kPastBytes;
   int rc;
   switch (a.dtype) {
     case FSDP_F32: rc = norm_grad_go<FSDP_F32>(go, a); break;

@@ -339,6 +339,7 @@ int norm_grad_impl(int32_t kind, int32_t n_ranks, int64_t rows, int64_t cols, in
   a.weight_dtype = weight_dtype;
   a.grad_dtype = grad_dtype;
   a.accumulate = accumulate != 0;
+  a.past_loads = a.past_stores = 0;
   const Timing t(stream);
   return launched(fsdp_launch_norm_grad(a, stream, t.start, t.stop), "norm_grad");
 }
