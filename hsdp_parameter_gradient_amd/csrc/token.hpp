@@ -73,6 +73,7 @@ struct NormArgs {
   uint64_t rows, cols;
   float eps, factor;
   int rms, dtype, weight_dtype;
+  int past_loads, past_y;  // past the caches (set by the launcher)
   Drop drop;
 };
 

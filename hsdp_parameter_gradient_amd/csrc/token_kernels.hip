@@ -932,11 +932,11 @@ __device__ __forceinline__ uint32_t group_len(uint64_t cols, uint32_t j) {
 // h - mean, less the square of what rounding the mean left: a row far from
 // zero loses nothing.
 //
-// Bound by HBM: 16384 x 4096 bf16 with residual 537 MB in 97 us, 5.5 TB/s
+// Bound by HBM: 16384 x 4096 bf16 with residual 537 MB in 95 us, 5.6 TB/s
 // (a plain copy: 6.4), the dropout hidden behind it; about 220 VALU
 // operations for 8 elements with it, half of what LDS shuffles, masks and
 // repeated conversions took before.
-template <int D, int LANES, int NV, bool DROP>
+template <int D, int LANES, int NV, bool DROP, bool PAST>
 __global__ __launch_bounds__(block_of(LANES)) void norm_kernel(fsdp::NormArgs a) {
   constexpr int kRows = block_of(LANES) / LANES;
   __shared__ float lds[2][2][LANES < 64 ? 1 : LANES / 64];
@@ -951,8 +951,8 @@ __global__ __launch_bounds__(block_of(LANES)) void norm_kernel(fsdp::NormArgs a)
     for (int i = 0; i < NV; ++i)
       if (len[i]) {
         const uint64_t at = r * a.cols + (uint64_t)(l + i * LANES) * kGroup;
-        x[i] = load_raw<D>(a.x, at, len[i]);
-        if (a.residual) res[i] = load_raw<D>(a.residual, at, len[i]);
+        x[i] = load_raw<D, PAST>(a.x, at, len[i]);
+        if (a.residual) res[i] = load_raw<D, PAST>(a.residual, at, len[i]);
       }
   };
 #pragma unroll
@@ -1030,7 +1030,11 @@ __global__ __launch_bounds__(block_of(LANES)) void norm_kernel(fsdp::NormArgs a)
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[i][k] = __builtin_fmaf(v[i][k] - rest, rstd * w[i][k], bias[i][k]);
-      if (len[i]) store_cols<D, 8>(a.y, at + (uint64_t)(l + i * LANES) * kGroup, len[i], v[i]);
+      if (!len[i]) continue;
+      if (a.past_y)
+        store_cols<D, 8, true>(a.y, at + (uint64_t)(l + i * LANES) * kGroup, len[i], v[i]);
+      else
+        store_cols<D, 8>(a.y, at + (uint64_t)(l + i * LANES) * kGroup, len[i], v[i]);
     }
   }
 }
@@ -1200,11 +1204,11 @@ __device__ __forceinline__ void sum_columns(const fsdp::NormGradArgs& a, const F
 // next row's loads are in flight while a row is computed.  Absent columns
 // load as dy = 0 and add nothing.
 //
-// Bound by HBM: 8 x 2048 x 4096 bf16 537 MB in 103 us, 5.2 TB/s; with dropout
-// 671 MB in 134 us.  LANES x NV is the fewest registers that hold a row: at
-// 4096 columns 512 x 1 (106 registers) 109 us a call, 256 x 2 (152) 120.
-// With dropout dres goes past the caches (143 -> 140 us): what is read next
-// is dx.
+// Bound by HBM: 8 x 2048 x 4096 bf16 with dropout 671 MB in 119 us a call, 5.6
+// TB/s.  LANES x NV is the fewest registers that hold a row: at 4096 columns
+// and without dropout 512 x 1 (106 registers) 109 us, 256 x 2 (152) 120.  With
+// dropout dres goes past the caches (143 -> 140 us): what is read next is dx.
+// PAST: the rows are loaded past the caches.
 //
 // FEW: a call of few rows in one launch.  The column sums need no row sum, so
 // workgroups of their own (the ones from row_blocks on) read dy and h once
@@ -1512,8 +1516,14 @@ int norm_rows(const Launch& go, const fsdp::NormArgs& a, uint64_t times) {
   constexpr int block = block_of(LANES);
   const uint64_t need = ceil_div(a.rows, block / LANES), most = times * 256 * (2048 / block);
   const dim3 grid((uint32_t)(need < most ? need : most));
-  if (a.drop.state) return go(norm_kernel<D, LANES, NV, true>, grid, block, true, true, a);
-  return go(norm_kernel<D, LANES, NV, false>, grid, block, true, true, a);
+  if constexpr (D != FSDP_F32) {
+    if (a.past_loads) {
+      if (a.drop.state) return go(norm_kernel<D, LANES, NV, true, true>, grid, block, true, true, a);
+      return go(norm_kernel<D, LANES, NV, false, true>, grid, block, true, true, a);
+    }
+  }
+  if (a.drop.state) return go(norm_kernel<D, LANES, NV, true, false>, grid, block, true, true, a);
+  return go(norm_kernel<D, LANES, NV, false, false>, grid, block, true, true, a);
 }
 
 template <int D>
@@ -1713,8 +1723,17 @@ int fsdp_launch_embedding_grad(const fsdp::EmbedGradArgs& a, void* stream, void*
   }
 }
 
-int fsdp_launch_norm(const fsdp::NormArgs& a, void* stream, void* start_event, void* stop_event) {
+int fsdp_launch_norm(const fsdp::NormArgs& args, void* stream, void* start_event, void* stop_event) {
   const Launch go = launch_of(stream, start_event, stop_event);
+  fsdp::NormArgs a = args;
+  // A call that moves more than the MALL holds reads x and the residual past
+  // the caches (where lines are not shared between rows); a y of the MALL's
+  // size is stored past them.  Measured on MI355X, bf16, us, with a copy of y
+  // behind the call (without these rules): 16384 x 4096 138 (154), 32768 x
+  // 4096 283 (299); a smaller y stored past them costs its reader: 144.
+  const uint64_t row = a.rows * a.cols * (a.dtype == FSDP_F32 ? 4 : 2);
+  a.past_loads = row * (2 + (a.residual != nullptr) + (a.h != nullptr)) >= kPastBytes && a.cols % kGroup == 0;
+  a.past_y = row >= kPastBytes;
   switch (a.dtype) {
     case FSDP_F32: return norm_go<FSDP_F32>(go, a);
     case FSDP_BF16: return norm_go<FSDP_BF16>(go, a);
@@ -1727,7 +1746,10 @@ int fsdp_launch_norm_grad(const fsdp::NormGradArgs& args, void* stream, void* st
   fsdp::NormGradArgs a = args;
   // A call that moves more than the MALL holds reads its rows, each for the
   // last time, past the caches, where lines are not shared between rows; one
-  // whose outputs alone fill the MALL also stores past them.
+  // whose outputs alone fill the MALL also stores past them.  Measured on
+  // MI355X, 8 ranks, bf16 with dropout, us, with a copy of dx behind the call
+  // (without the loads' rule, without both): 8192 x 4096 84 (97), 16384 x
+  // 4096 165 (169, 191).
   const uint64_t row = a.rows * (uint64_t)a.n_ranks * a.cols * (a.dtype == FSDP_F32 ? 4 : 2);
   const uint64_t outs = row * (a.dx ? 2 : 1), ins = row * (a.dh ? 3 : 2);
   a.past_loads = ins + outs >= kPastBytes && a.cols % kGroup == 0;

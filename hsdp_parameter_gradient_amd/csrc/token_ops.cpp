@@ -260,6 +260,7 @@ int norm_impl(int32_t kind, int64_t rows, int64_t cols, int32_t dtype, int32_t w
   a.rms = kind == FSDP_RMS_NORM;
   a.dtype = dtype;
   a.weight_dtype = weight_dtype;
+  a.past_loads = a.past_y = 0;
   const Timing t(stream);
   return launched(fsdp_launch_norm(a, stream, t.start, t.stop), "norm");
 }

@@ -494,6 +494,49 @@ def test_seed_step_and_site_change_the_mask():
     assert set(top.unique().tolist()) <= {0.0, 65536.0}
 
 
+@pytest.mark.parametrize("residual", [False, True])
+def test_large_calls_give_the_bits_of_small_ones(residual):
+    """Calls that move more than the MALL holds load and store past the caches:
+    the same bits as calls on a part of their rows (a rank of its own each)."""
+    require_gpu()
+    note(f"[large] residual={residual}")
+    E, n, part = 1024, 140000, 20000  # 287 MB a tensor of bf16
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(31)
+    x, res, dy = (torch.randn(n, E, device="cuda", generator=gen).to(torch.bfloat16) for _ in range(3))
+    res = res if residual else None
+    w, b = torch.randn(E, device="cuda"), torch.randn(E, device="cuda")
+    h = torch.empty_like(x) if residual else None
+    y, mean, rstd = torch.empty_like(x), torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    hp.fsdp_norm(x, w, y, bias=b, residual=res, h=h, mean=mean, rstd=rstd)
+    R = n // part
+    gw, gb = ([torch.empty(E, device="cuda") for _ in range(R)] for _ in range(2))
+    dres, dx = torch.empty_like(x), torch.empty_like(x)
+    hv = h if residual else x
+    hp.fsdp_norm_grad(dy, hv, rstd, w, dres, gw, mean=mean, dbias=gb, dh=res, dx=dx)
+    out = torch.empty_like(x)
+    tok = torch.randint(-1, 5000, (n,), device="cuda", generator=gen)
+    hp.fsdp_embedding(tok, x[:5000], out, scale=0.5)
+    assert torch.equal(out, torch.where((tok >= 0)[:, None], x[tok.clamp_min(0)] * 0.5, 0.0).to(out.dtype))
+    for k in (0, 3, R - 1):
+        at = slice(k * part, (k + 1) * part)
+        o = {m: torch.empty(part, E, dtype=torch.bfloat16, device="cuda") for m in ("h", "y", "dres", "dx")}
+        m1, r1 = torch.empty(part, device="cuda"), torch.empty(part, device="cuda")
+        hp.fsdp_norm(x[at], w, o["y"], bias=b, residual=None if res is None else res[at],
+                     h=o["h"] if residual else None, mean=m1, rstd=r1)
+        assert torch.equal(o["y"], y[at]) and torch.equal(m1, mean[at]) and torch.equal(r1, rstd[at])
+        assert not residual or torch.equal(o["h"], h[at])
+        w1, b1 = torch.empty(E, device="cuda"), torch.empty(E, device="cuda")
+        hp.fsdp_norm_grad(dy[at], hv[at], r1, w, o["dres"], [w1], mean=m1, dbias=[b1],
+                          dh=None if res is None else res[at], dx=o["dx"])
+        assert torch.equal(o["dres"], dres[at]) and torch.equal(o["dx"], dx[at]) and torch.equal(o["dx"], o["dres"])
+        # the column sums' order goes by the ranks' workgroups: each side within (n + 8) U of sum|terms|
+        d = dy[at].double().abs()
+        xh = ((hv[at].double() - m1.double()[:, None]) * r1.double()[:, None]).abs()
+        for one, of, size in ((w1, gw[k], (d * xh).sum(0)), (b1, gb[k], d.sum(0))):
+            assert bool(((one - of).abs() <= 2 * (part + 8) * U * size).all())
+
+
 # --- addresses -------------------------------------------------------------------
 
 def test_offsets_beyond_32_bits():
