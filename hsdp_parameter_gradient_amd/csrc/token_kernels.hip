@@ -585,8 +585,8 @@ __device__ __forceinline__ void zero_block(const fsdp::EmbedGradArgs& a, void* g
 // it empty rows) in 607 us, 6.7 TB/s; in plain workgroup order 635, with 8
 // blocks a lane 655, 2 a lane 717, nontemporal stores 702, and in the launch
 // that sums the rows 790 for both (607 + 88 apart).
-__global__ __launch_bounds__(kFillBlock) void embedding_fill_kernel(fsdp::EmbedGradArgs a, fsdp::RankPtrs grads, uint32_t rank0,
-                                          GradGrid grid) {
+__global__ __launch_bounds__(kFillBlock) void embedding_fill_kernel(fsdp::EmbedGradArgs a, fsdp::RankPtrs grads,
+                                                                    uint32_t rank0, GradGrid grid) {
   const RankView rv = rank_view(a, rank0 + blockIdx.y);
   constexpr uint32_t kItems = kFillBlock * kFillUnroll;
   const uint64_t first = (uint64_t)xcd_order<kFillRun>(blockIdx.x, gridDim.x) * kItems;
@@ -1627,8 +1627,8 @@ int embedding_grad_go(const Launch& go, const fsdp::EmbedGradArgs& a) {
     for (int g0 = 0; g0 < a.n_ranks; g0 += fsdp::kMaxRankPtrs) {
       const int n = a.n_ranks - g0 < fsdp::kMaxRankPtrs ? a.n_ranks - g0 : fsdp::kMaxRankPtrs;
       const fsdp::RankPtrs ptrs = rank_ptrs(a.grads, g0, n);
-      const int rc = go(embedding_grad_small_kernel<D, DROP, ADD>, dim3((uint32_t)p.small, (uint32_t)n), kSmallBlock, g0 == 0,
-                        g0 + n == a.n_ranks, a, ptrs, (uint32_t)g0, grid);
+      const int rc = go(embedding_grad_small_kernel<D, DROP, ADD>, dim3((uint32_t)p.small, (uint32_t)n), kSmallBlock,
+                        g0 == 0, g0 + n == a.n_ranks, a, ptrs, (uint32_t)g0, grid);
       if (rc) return rc;
     }
     return 0;
@@ -1701,8 +1701,8 @@ bool fsdp::embedding_fits(uint64_t n_tokens, uint64_t cols) {
 
 bool fsdp::embedding_grad_fits(uint64_t n_tokens, uint64_t vocab, uint64_t cols, int n_ranks) {
   const GradPlan p = grad_plan(n_tokens, vocab, cols, n_ranks, 4, false);
-  return grid_fits(p.sort, kSortBlock) && grid_fits(p.piece_blocks, kGradBlock) && grid_fits(p.fill, kFillBlock) && grid_fits(p.small, kSmallBlock) &&
-         grid_fits(p.join_blocks, kJoinBlock);
+  return grid_fits(p.sort, kSortBlock) && grid_fits(p.piece_blocks, kGradBlock) && grid_fits(p.fill, kFillBlock) &&
+         grid_fits(p.small, kSmallBlock) && grid_fits(p.join_blocks, kJoinBlock);
 }
 
 int fsdp_launch_embedding(const fsdp::EmbedArgs& a, void* stream, void* start_event, void* stop_event) {

@@ -269,6 +269,7 @@ int norm_workspace(int32_t n_ranks, int64_t rows, int64_t cols, int* blocks, int
   int rc;
   if ((rc = check_ranks(n_ranks)) || (rc = check_count(rows, 0, "rows")) || (rc = check_count(cols, 1, "cols")))
     return rc;
+  if (cols >= int64_t(1) << 28) return fail(FSDP_EINVAL, "cols %lld: the gradient takes fewer than 2^28", (long long)cols);
   *blocks = fsdp::norm_grad_blocks(rows, cols, n_ranks);
   if (fsdp::norm_grad_few(rows, cols, n_ranks)) {
     *bytes = 0;

@@ -35,8 +35,8 @@ def _ptr(t: torch.Tensor, what: str, numel: int, dtype: Optional[torch.dtype], d
     empty), after the checks of _binding._dev and that it is on `device`.
     These calls are short: the checks that pass cost as little as they can."""
     try:
-        if t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype) and t.numel() == numel and \
-                t.get_device() == device:
+        if t.get_device() == device and t.is_contiguous() and (dtype is None or t.dtype is dtype) and \
+                t.numel() == numel:  # a host tensor's device is -1
             return t.data_ptr() if numel else None
     except AttributeError:
         pass

@@ -3,8 +3,9 @@
  *
  * One bucket of P parameters, sharded (on dim 0 unless a parameter states
  * another dim) over a shard group of S ranks and replicated over D = R / S
- * replicate groups, R simulated ranks resident in one GPU's HBM.  Every device entry point of that path is one HIP kernel
- * launch, enqueued on the caller's stream.  A call whose descriptor table (a
+ * replicate groups, R simulated ranks resident in one GPU's HBM.  Every
+ * device entry point of that path is one HIP kernel launch, enqueued on the
+ * caller's stream.  A call whose descriptor table (a
  * function of its shapes, sizes and pointers) is new uploads that table
  * once with a blocking copy; a repeated call makes no HIP call besides the
  * launch and does not synchronise the host.
@@ -49,10 +50,10 @@
  *     fsdp_fused_ar, which works in place by definition.
  *   - Padding is written as zero on every call; no output needs to be
  *     cleared beforehand.
- *   - The library caches a plan per call signature of the flat-buffer entry
- *     points (the token operators have none; entry point, sizes,
- *     shapes, shard dims, pointers, device): the call's descriptor table in
- *     device memory and its launch parameters.  A repeated call launches its
+ *   - The library caches a plan per call signature (entry point, sizes,
+ *     shapes, shard dims, pointers, device) of the flat-buffer entry points:
+ *     the call's descriptor table in device memory and its launch parameters
+ *     (the token operators have neither).  A repeated call launches its
  *     plan without validating or planning again (its result cannot differ).
  *     At most 256 plans and 256 MiB of tables; evicting waits for every
  *     device that holds a cached table.  fsdp_release_cache() frees them all.
@@ -377,6 +378,7 @@ int fsdp_norm(int32_t kind, int64_t rows, int64_t cols, int32_t dtype, int32_t w
  * dres is the gradient of h, so also of the residual; dx that of x.  dh is
  * what reaches h past the norm, through the residual stream.
  *   rows           of one rank: every row buffer has n_ranks * rows of them
+ *   cols           below 2^28
  *   dh, dx, dbias  may be NULL (dx not with a dropout)
  *   mean           read for FSDP_LAYER_NORM only
  *   dweight, dbias [n_ranks] device pointers (host arrays), cols of grad_dtype

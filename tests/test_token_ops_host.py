@@ -159,6 +159,7 @@ REFUSED = [
     ("fsdp_norm_grad", dict(dx=BASE + (6 << 32)), 5), ("fsdp_norm_grad", dict(rows=600, workspace_bytes=16), 1),
     ("fsdp_norm_grad", dict(rows=600, workspace=None), 1), ("fsdp_norm_grad", dict(dweight=_ptrs([0, BASE + (8 << 32)])), 1),
     ("fsdp_norm_grad", dict(rows=1 << 30, n_ranks=8, dropout=_drop()), 1),
+    ("fsdp_norm_grad", dict(rows=0, cols=1 << 28), 1),
 ]
 
 
